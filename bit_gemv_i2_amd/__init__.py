@@ -99,7 +99,27 @@ _SIGS = {
                                          ctypes.c_void_p], ctypes.c_int),
     "bitnet_w2a8_chain_static": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
                                   ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "bitnet_kv_cache_bytes": ([ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int], ctypes.c_size_t),
+    "bitnet_rope_table": ([ctypes.c_int64, ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.c_int64,
+                           ctypes.c_void_p], ctypes.c_int),
+    "bitnet_rope_append_kv": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                               ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                               ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 4, ctypes.c_int),
+    "bitnet_attn_decode_workspace_bytes": ([ctypes.c_int] * 5, ctypes.c_size_t),
+    "bitnet_attn_decode": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                            ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                            ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "bitnet_attn_prompt": ([ctypes.c_void_p, ctypes.c_int64] * 3 + [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64]
+                           + [ctypes.c_int] * 5 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
 }
+
+
+class KVCacheStruct(ctypes.Structure):
+    """bitnet_kv_cache_t"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page", ctypes.c_int),
+                ("batch", ctypes.c_int), ("slots", ctypes.c_int)]
 
 
 class ChainLayer(ctypes.Structure):
@@ -524,7 +544,201 @@ def bitnet_w2a8_gemv_lut(packed, scales, q, s_a, N: int, K: int, tiles_per_group
     return (y, acc) if acc is not None else y
 
 
+# ------------------------------------------------------------------ attention side of a decoder layer
+def bitnet_kv_cache_bytes(pages: int, kv_heads: int, head_dim: int, page: int) -> int:
+    return lib().bitnet_kv_cache_bytes(int(pages), int(kv_heads), int(head_dim), int(page))
+
+
+def bitnet_rope_table(positions: int, rot: int, base: float = 10000.0, factor: float = 1.0, trained: int = 0):
+    """Rotary table, fp32 numpy [positions][rot] (cosines, then sines).  factor > 1 stretches the
+    positions: all rates by 1/factor, or by parts when `trained` gives the context length of the training."""
+    if positions < 1 or rot < 1:
+        raise BitnetError(BITNET_ERR_UNSUPPORTED_SHAPE, "bitnet_rope_table")
+    t = np.empty((positions, rot), np.float32)
+    _ok(lib().bitnet_rope_table(int(positions), int(rot), float(base), float(factor), int(trained), _np_ptr(t)),
+        "bitnet_rope_table")
+    return t
+
+
+def _cache_struct(k_cache, v_cache, k_scale, v_scale, table):
+    """bitnet_kv_cache_t over the given tensors, each checked against the layout of the header."""
+    import torch
+    if k_cache.dim() != 4 or table.dim() != 2:
+        raise ValueError("k_cache must be [pages][kv_heads][page][head_dim] and table [batch][slots]")
+    pages, heads, page, dim = k_cache.shape
+    _check(k_cache, "k_cache", torch.int8)
+    _check(v_cache, "v_cache", torch.int8, shape=(pages, heads, dim, page))
+    _check(k_scale, "k_scale", torch.float32, shape=(pages, heads))
+    _check(v_scale, "v_scale", torch.float32, shape=(pages, heads))
+    _check(table, "table", torch.int32)
+    return KVCacheStruct(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
+                         _dev_ptr(v_scale, "v_scale"), _dev_ptr(table, "table"), pages, heads, dim, page,
+                         table.shape[0], table.shape[1])
+
+
+def _rows_ptr(t, name: str, inner: int):
+    """(pointer, elements from row to row) of a device tensor whose rows hold `inner` elements side by side:
+    contiguous, or a slice of wider rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    want = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != want:
+            raise ValueError(f"{name} must have its heads and channels side by side in a row")
+        want *= size
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else inner
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream`, taken from that stream's pool so that nothing still pending elsewhere
+    uses it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _float_dt(t, name: str) -> int:
+    import torch
+    dt = {torch.bfloat16: BITNET_DT_BF16, torch.float32: BITNET_DT_F32}.get(t.dtype if hasattr(t, "dtype") else t)
+    if dt is None:
+        raise ValueError(f"{name} must be bf16 or fp32")
+    return dt
+
+
+def bitnet_rope_append_kv(qkv, rope, k_cache, v_cache, k_scale, v_scale, table, starts, before, max_new: int,
+                          q_heads: int, interleaved: bool = False, with_k: bool = False, q_out=None, k_out=None,
+                          stream=None):
+    """Turns the queries and keys of the fused projection qkv [T][(q_heads + 2 kv_heads) * head_dim] by their
+    positions and appends keys and values to the paged int8 cache.  rope: fp32 [positions][rot] on the device, or
+    None; starts int32 [batch + 1], before int32 [batch].  Returns (q [T][q_heads][head_dim], k or None); k,
+    the turned keys, is made when with_k or k_out asks for it."""
+    import torch
+    c = _cache_struct(k_cache, v_cache, k_scale, v_scale, table)
+    dt = _float_dt(qkv, "qkv")
+    width = (q_heads + 2 * c.kv_heads) * c.head_dim
+    if qkv.dim() != 2 or qkv.shape[1] != width:
+        raise ValueError(f"qkv must be [T][{width}], not {tuple(qkv.shape)}")
+    T = qkv.shape[0]
+    _check(starts, "starts", torch.int32, shape=(c.batch + 1,))
+    _check(before, "before", torch.int32, shape=(c.batch,))
+    rot = rows = 0
+    rp = None
+    if rope is not None:
+        _check(rope, "rope", torch.float32)
+        if rope.dim() != 2:
+            raise ValueError("rope must be [positions][rot]")
+        rows, rot = rope.shape
+        rp = _dev_ptr(rope, "rope")
+    xp, stride = _rows_ptr(qkv, "qkv", width)
+    if q_out is None:
+        q_out = _empty((T, q_heads, c.head_dim), qkv.dtype, qkv.device, stream)
+    if k_out is None and with_k:
+        k_out = _empty((T, c.kv_heads, c.head_dim), qkv.dtype, qkv.device, stream)
+    _check(q_out, "q_out", qkv.dtype, numel=T * q_heads * c.head_dim)
+    kp = None
+    if k_out is not None:
+        _check(k_out, "k_out", qkv.dtype, numel=T * c.kv_heads * c.head_dim)
+        kp = _dev_ptr(k_out, "k_out")
+    _ok(lib().bitnet_rope_append_kv(xp, dt, stride, rp, rows, rot, int(bool(interleaved)), _dev_ptr(starts, "starts"),
+                                    _dev_ptr(before, "before"), T, int(max_new), int(q_heads), ctypes.byref(c),
+                                    _dev_ptr(q_out, "q_out"), kp, _stream(stream)), "bitnet_rope_append_kv")
+    return q_out, k_out
+
+
+def bitnet_attn_decode_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int) -> int:
+    return lib().bitnet_attn_decode_workspace_bytes(int(batch), int(q_heads), int(kv_heads), int(head_dim),
+                                                    int(max_len))
+
+
+def bitnet_attn_decode(q, k_cache, v_cache, k_scale, v_scale, table, lengths, max_len: int, scale: float | None = None,
+                       out=None, out_dtype=None, workspace=None, stream=None):
+    """Attention of one query token per sequence, q [batch][q_heads][head_dim], over the paged int8 cache; `lengths`
+    int32 [batch] counts the cached tokens, max_len bounds them.  scale defaults to 1/sqrt(head_dim).  Returns
+    [batch][q_heads][head_dim] in out_dtype (q's by default).  The workspace is allocated unless given."""
+    import torch
+    c = _cache_struct(k_cache, v_cache, k_scale, v_scale, table)
+    qdt = _float_dt(q, "q")
+    if q.dim() != 3 or q.shape[0] != c.batch or q.shape[2] != c.head_dim:
+        raise ValueError(f"q must be [{c.batch}][q_heads][{c.head_dim}], not {tuple(q.shape)}")
+    hq = q.shape[1]
+    _check(lengths, "lengths", torch.int32, shape=(c.batch,))
+    if out is None:
+        out = _empty((c.batch, hq, c.head_dim), out_dtype or q.dtype, q.device, stream)
+    odt = _float_dt(out, "out")
+    _check(out, "out", out_dtype or out.dtype, numel=c.batch * hq * c.head_dim)
+    need = lib().bitnet_attn_decode_workspace_bytes(c.batch, hq, c.kv_heads, c.head_dim, int(max_len))
+    wp, nb = None, 0
+    if workspace is None and need:
+        workspace = _empty((need,), torch.uint8, q.device, stream)
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8)
+        wp, nb = _dev_ptr(workspace, "workspace"), workspace.numel()
+        if nb < need:
+            raise ValueError(f"workspace must hold at least {need} bytes")
+    qp, stride = _rows_ptr(q, "q", hq * c.head_dim)
+    _ok(lib().bitnet_attn_decode(qp, qdt, stride, ctypes.byref(c), _dev_ptr(lengths, "lengths"), int(max_len), hq,
+                                 c.head_dim ** -0.5 if scale is None else float(scale), _dev_ptr(out, "out"), odt, wp, nb,
+                                 _stream(stream)), "bitnet_attn_decode")
+    return out
+
+
+def bitnet_attn_prompt(q, k, v, starts, max_len: int, causal: bool = True, scale: float | None = None, out=None,
+                       stream=None):
+    """Attention over whole prompts packed one behind the other: q [T][q_heads][head_dim], k and v
+    [T][kv_heads][head_dim], bf16, tokens at any stride; starts int32 [batch + 1], max_len the longest prompt.
+    Returns bf16 [T][q_heads][head_dim]."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or v.shape != k.shape:
+        raise ValueError("q must be [T][q_heads][head_dim], k and v [T][kv_heads][head_dim]")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _check(t, name, torch.bfloat16)
+    _check(starts, "starts", torch.int32)
+    if starts.dim() != 1 or starts.shape[0] < 2:
+        raise ValueError("starts must be [batch + 1]")
+    T, hq, dim = q.shape
+    hk = k.shape[1]
+    if out is None:
+        out = _empty((T, hq, dim), torch.bfloat16, q.device, stream)
+    _check(out, "out", torch.bfloat16, numel=T * hq * dim)
+    qp, qs = _rows_ptr(q, "q", hq * dim)
+    kp, ks = _rows_ptr(k, "k", hk * dim)
+    vp, vs = _rows_ptr(v, "v", hk * dim)
+    _ok(lib().bitnet_attn_prompt(qp, qs, kp, ks, vp, vs, _dev_ptr(starts, "starts"), starts.shape[0] - 1, T,
+                                 int(max_len), hq, hk, dim, int(bool(causal)),
+                                 dim ** -0.5 if scale is None else float(scale), _dev_ptr(out, "out"), _stream(stream)),
+        "bitnet_attn_prompt")
+    return out
+
+
 # ------------------------------------------------------------------ convenience
+@dataclass
+class KVCache:
+    """A paged int8 cache resident in device memory, in the layout of bitnet_kv_cache_t."""
+    k: object        # torch int8 [pages][kv_heads][page][head_dim]
+    v: object        # torch int8 [pages][kv_heads][head_dim][page]
+    k_scale: object  # torch fp32 [pages][kv_heads]
+    v_scale: object
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda"):
+        import torch
+        if bitnet_kv_cache_bytes(pages, kv_heads, head_dim, page) == 0:
+            raise BitnetError(BITNET_ERR_UNSUPPORTED_SHAPE, "bitnet_kv_cache_bytes")
+        return cls(torch.zeros((pages, kv_heads, page, head_dim), dtype=torch.int8, device=device),
+                   torch.zeros((pages, kv_heads, head_dim, page), dtype=torch.int8, device=device),
+                   torch.zeros((pages, kv_heads), dtype=torch.float32, device=device),
+                   torch.zeros((pages, kv_heads), dtype=torch.float32, device=device))
+
+    def append(self, qkv, rope, table, starts, before, max_new, q_heads, **kw):
+        return bitnet_rope_append_kv(qkv, rope, self.k, self.v, self.k_scale, self.v_scale, table, starts, before,
+                                     max_new, q_heads, **kw)
+
+    def attend(self, q, table, lengths, max_len, **kw):
+        return bitnet_attn_decode(q, self.k, self.v, self.k_scale, self.v_scale, table, lengths, max_len, **kw)
+
+
 @dataclass
 class PackedWeight:
     """A ternary weight matrix resident in device memory in the tile layout."""

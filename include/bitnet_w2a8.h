@@ -415,6 +415,126 @@ bitnet_status_t bitnet_w2a8_gemv_lut(const uint8_t *packed, const float *scales,
                                      const float *s_a, float *y, int32_t *acc, int N, int K,
                                      int tiles_per_group, hipStream_t stream);
 
+/* ---------------------------------------------------------------- attention side of a decoder layer
+ *
+ * What stands between the fused query/key/value product of a layer and its output
+ * product: rotary positions, a paged int8 cache of keys and values, attention of one
+ * token per sequence over that cache, and attention over whole prompts.
+ *
+ * Heads: q_heads query heads share kv_heads key heads in groups of q_heads / kv_heads
+ * (query head i reads key head i / (q_heads / kv_heads)); head_dim is 64 or 128.
+ *
+ * Paged cache.  A page holds `page` consecutive positions of one sequence (16, 32, 64
+ * or 128) for every key head, as int8 codes with one fp32 scale per page and head
+ * for the keys and one for the values (value = code * scale):
+ *     k        int8 [pages][kv_heads][page][head_dim]
+ *     v        int8 [pages][kv_heads][head_dim][page]   (positions fastest: the order in
+ *              which the matrix cores take them, so that attention reads 16 positions of one
+ *              channel as one 16-byte piece)
+ *     k_scale, v_scale  fp32 [pages][kv_heads]
+ *     table    int32 [batch][slots]: table[b][i] is the page of positions
+ *              i * page .. i * page + page - 1 of sequence b.  Entries past a sequence's
+ *              end are not read.  An entry outside 0 .. pages - 1 is never followed:
+ *              nothing is stored there, and attention sees no token of that page.
+ * A page belongs to one sequence while it is appended to; sequences may share pages that
+ * are only read.  Scales are finite and >= 0. */
+typedef struct {
+    int8_t *k, *v;
+    float *k_scale, *v_scale;
+    const int32_t *table;
+    int64_t pages;
+    int kv_heads, head_dim, page;
+    int batch, slots;
+} bitnet_kv_cache_t;
+
+/* Bytes of the key codes (and of the value codes) of a cache: pages * kv_heads * page *
+ * head_dim; 0 if the page or head size is not one of those above or a count is < 1. */
+size_t bitnet_kv_cache_bytes(int64_t pages, int kv_heads, int head_dim, int page);
+
+/* Rotary table (host): row p holds cos(p * r_j), j = 0 .. rot/2 - 1, then the rot/2 sines, in
+ * fp64 rounded once to fp32, with rates r_j = base^(-2j / rot).  For contexts longer than
+ * those a model was trained on, factor > 1 slows the rates: all of them by 1/factor when
+ * trained = 0 (positions interpolated linearly); with trained > 0, the context length of the training,
+ * each by its number of turns n_j = trained * r_j / (2 pi) (interpolation by parts; Peng et al.,
+ * "YaRN: Efficient Context Window Extension of Large Language Models", 2023): 1/factor where
+ * n_j < 1, unchanged where n_j > 32, linear in n_j between.
+ *   table  host, fp32 [positions][rot] (out)
+ * Rules: positions >= 1, rot % 16 == 0 and 16 <= rot <= 128 (else UNSUPPORTED_SHAPE); base > 1,
+ * factor >= 1, both finite, trained >= 0 (else INVALID_ARG). */
+bitnet_status_t bitnet_rope_table(int64_t positions, int rot, double base, double factor, int64_t trained,
+                                  float *table);
+
+/* Rotary positions on the queries and keys of a fused projection, and the new keys and
+ * values appended to the paged cache, in one launch.  Token t of sequence b, starts[b] <= t <
+ * starts[b+1], has position p = before[b] + t - starts[b].
+ *   Turn: in the first rot channels of a head the pair (x0, x1) becomes (x0 c - x1 s, x1 c + x0 s),
+ *   each product and sum rounded by itself in fp32, c and s from row p of `rope`.  Pairs are
+ *   (i, i + rot/2), or (2i, 2i + 1) when `interleaved`.  Channels >= rot stay.
+ *   Store: keys from the turned fp32 values, values from the projection.  Per page and
+ *   head, with amax over the new tokens of that page, the scale becomes max(amax, 1e-5) / 127, or
+ *   the old scale if that is larger and the page already holds older tokens; then the older
+ *   codes, if their scale grew, become rint(code * (old / new)); a new code is
+ *   clamp(rint(x * (1 / scale)), -127, 127).  (fp32, half to even, correctly rounded divisions.)
+ *   Codes of positions that no token has yet are left as they are.
+ *   qkv      device, [tokens][(q_heads + 2 kv_heads) * head_dim], queries, keys, values;
+ *            dt BITNET_DT_BF16 or BITNET_DT_F32; rows `row_stride` elements apart
+ *   rope     device, fp32 [rope_rows][rot] (bitnet_rope_table)
+ *   starts   device, int32 [batch + 1];  before  device, int32 [batch] (tokens in the cache)
+ *   max_new  the most new tokens a sequence has; of a longer one only the first max_new are
+ *            handled
+ *   q_out    device, [tokens][q_heads][head_dim] of dt: the turned queries (out)
+ *   k_out    the same for the keys, [tokens][kv_heads][head_dim], or NULL (prompt attention reads it)
+ * q_out and k_out must not overlap qkv.  A token past the positions that a row of `table`
+ * can name (slots * page) is not stored and its q_out and k_out rows are zero.
+ * Rules: head_dim, page as above; rot % 16 == 0, 0 <= rot <= head_dim (rot 0: no turn, rope
+ * may be NULL); rope_rows >= slots * page; row_stride >= the row and a multiple of 8; tokens,
+ * max_new, batch, slots, pages >= 1; batch <= 65535; tokens <= 2^24; kv_heads divides q_heads <= 1024
+ * (else UNSUPPORTED_SHAPE).  Pointers 16-byte aligned (starts, before, table: 4). */
+bitnet_status_t bitnet_rope_append_kv(const void *qkv, int dt, int64_t row_stride, const float *rope,
+                                      int64_t rope_rows, int rot, int interleaved, const int32_t *starts,
+                                      const int32_t *before, int64_t tokens, int max_new, int q_heads,
+                                      const bitnet_kv_cache_t *cache, void *q_out, void *k_out, hipStream_t stream);
+
+/* Attention of one token per sequence over the paged cache:
+ *     out[b][i] = sum_j softmax_j(scale * q[b][i] . k_j) v_j,   j < lengths[b]
+ * with k_j, v_j the values that the codes stand for.  The products run on the int8
+ * matrix cores on the codes as they lie: a query row and the softmax weights of 64 positions are
+ * taken as sums of int8 digits to the base 256 (q: 22 bits below the row's largest for bf16, 30 for fp32;
+ * weights: 15 bits below the largest of their 64 for a bf16 output, 23 for fp32),
+ * summed exactly in int32; statistics and sums over blocks are fp32.
+ *   q          device, [batch][q_heads][head_dim], qdt BITNET_DT_BF16 or BITNET_DT_F32, sequences
+ *              `q_stride` elements apart
+ *   lengths    device, int32 [batch]: tokens in the cache, the current one included; a length
+ *              above max_len or slots * page is read as that, one below 1 gives zeros
+ *   out        device, [batch][q_heads][head_dim], odt BITNET_DT_BF16 or BITNET_DT_F32
+ *   workspace  device, 256-byte aligned, >= bitnet_attn_decode_workspace_bytes(...); clobbered; may
+ *              be NULL where that is 0
+ * Rules: the cache's; scale > 0 and finite; q_stride >= q_heads * head_dim and a multiple of 8;
+ * kv_heads divides q_heads <= 1024; batch <= 65535; max_len >= 1. */
+size_t bitnet_attn_decode_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim, int max_len);
+bitnet_status_t bitnet_attn_decode(const void *q, int qdt, int64_t q_stride, const bitnet_kv_cache_t *cache,
+                                   const int32_t *lengths, int max_len, int q_heads, float scale, void *out, int odt,
+                                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Attention over whole prompts, packed one behind the other: sequence b is rows
+ * starts[b] .. starts[b+1] - 1 of q, k, v and out;
+ *     out[t][i] = sum_u softmax_u(scale * q[t][i] . k[u]) v[u]
+ * over the u of the same sequence, u <= t when causal.  bf16 in and out; scores, softmax
+ * statistics and sums are fp32, the weights are rounded to bf16 for the matrix cores (their
+ * sum is taken before that rounding).
+ *   q        device, bf16 [tokens][q_heads][head_dim], tokens q_stride elements apart
+ *   k, v     device, bf16 [tokens][kv_heads][head_dim], tokens k_stride / v_stride elements
+ *            apart (views of a fused projection are read in place)
+ *   starts   device, int32 [batch + 1]
+ *   max_len  the longest sequence; of a longer one only the first max_len rows take part
+ *   out      device, bf16 [tokens][q_heads][head_dim]; rows of no sequence are not written
+ * out must not overlap q, k or v.  Rules: strides >= the row and multiples of 8; scale > 0 and finite;
+ * head_dim 64 or 128; kv_heads divides q_heads <= 1024; batch <= 65535; 1 <= tokens <= 2^24. */
+bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                   int64_t v_stride, const int32_t *starts, int batch, int64_t tokens, int max_len,
+                                   int q_heads, int kv_heads, int head_dim, int causal, float scale, void *out,
+                                   hipStream_t stream);
+
 /* ---------------------------------------------------------------- measurement helper */
 
 /* Not part of the product path: one pass of 16-byte non-temporal (streaming)
