@@ -5,16 +5,17 @@
 //
 // Matrix-core formulation.  v_mfma_i32_16x16x64_i8 takes the codes as they lie in memory, with
 // no conversion: a tile of 64 tokens is S^T = K Q^T (16 tokens x 64 channels by 64 channels x
-// 16 query rows) and O^T = V^T P^T (16 channels x 64 tokens by 64 tokens x 16 query rows).  The other
-// operand has to be int8 too, so a query row and a tile's softmax weights are written as a
-// few int8 digits to the base 256 under one scale, one product per digit; sums of digits are exact
-// in int32 (64 * 127 * 128 < 2^21, 128 * 128 * 128 = 2^21).
+// 16 columns) and O^T = V^T P^T (16 channels x 64 tokens by 64 tokens x 16 columns).  The other operand has
+// to be int8 too, so a query row and a tile's softmax weights are written as int8 digits to the
+// base 256 under one scale, and the 16 columns are 4 query heads x 4 digits: few heads share a key head, so the columns
+// are there, and one product does for all digits.  Sums of digits are exact in int32 (64 * 127 * 128 < 2^21,
+// 128 * 128 * 128 = 2^21); the digits of a score meet in two adds inside a quad of lanes, those of the output
+// once, at the end.  q: 30 bits below the row's largest; weights: 23 bits below the largest of their tile.
 //
 // Lane l = 16g + c of a result holds rows 4g .. 4g+3 of column c.  The rows of the four score
 // tiles are taken from the tokens 16 (i / 4) + 4 tt + i % 4, so that lane (g, c) receives the scores of
-// the 16 consecutive tokens 16g .. 16g+15 for query row c: exactly the 16 bytes of the second
+// the 16 consecutive tokens 16g .. 16g+15: exactly the 16 bytes of the second
 // product's operand that this lane has to supply, and tokens of one page (a page is a multiple of 16).
-// Nothing moves between lanes but the maxima of a row.
 //
 // A query row whose tile has maximum mt takes e_j = exp(s_j - mt) <= 1, digits of e_j under
 // the tile's own maximum, and joins the running sums with exp(mt - m): a tile far below the
@@ -26,14 +27,24 @@
 #include "attention.h"
 #include "bitnet_w2a8.h"
 
+// The four lanes of a quad take their digits from their own copies of a weight, which must agree to the last bit: no
+// product may be fused into one lane's sum and not into the other's.
+#pragma clang fp contract(off)
+
 using namespace bitnet_attn;
 
 namespace {
 
 constexpr int kWaves = 4;       // waves of a workgroup, which take its tiles in turn
 constexpr int kTile = 64;       // tokens of a tile: one int8 product's depth
-constexpr int kCols = 16;       // query rows of a product
-constexpr int kWantGroups = 512;  // workgroups that a launch is split into where the contexts allow
+// Workgroups that a launch is split into where the contexts allow: 2 for each of 256 CUs, as many as the registers let
+// reside.  (131071 tokens, 20 / 5 heads of 128: 34.9 us, 768 35.4, 1024 37.5, and a longer join.)
+constexpr int kWantGroups = 512;
+// Caches of more bytes than the memory-side cache holds are read past it (non-temporal loads): 1.07 GB in 171 us
+// instead of 187, 98% of a bare read's rate; 42 MB, which that cache keeps from call to call, in 14.4 us, but 17.2
+// so.  Not for pages of 128: a tile takes half of each 128-byte line of values, and the line has to stay for the
+// other half (1.07 GB: 187 us, but 221 so).
+constexpr int64_t kStreamBytes = 256ll << 20;
 
 struct DecodeArgs {
     const void *q;
@@ -43,6 +54,7 @@ struct DecodeArgs {
     const int32_t *table, *lengths;
     int64_t pages;
     int kv_heads, q_heads, group, page, page_shift, slots, max_len;
+    int q_bf16, out_bf16;
     int chunk;    // tiles of one workgroup
     int splits;   // workgroups along the longest context
     float scale2; // scale * log2(e)
@@ -54,62 +66,53 @@ __device__ __forceinline__ v4i mfma_i8(v4i a, v4i b, v4i c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// Byte i of each of four words, as one word.
-template <int I>
-__device__ __forceinline__ uint32_t gather_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    const uint32_t sel = 0x0C0C0000u | (uint32_t)((4 + I) << 8) | (uint32_t)I;
-    const uint32_t lo = __builtin_amdgcn_perm(b, a, sel);
-    const uint32_t hi = __builtin_amdgcn_perm(d, c, sel);
-    return lo | (hi << 16);
+// One byte of each of four words, as one word.  sel: the byte's number in its second, 4 more in its
+// second lowest byte, or 0x0C in both for zeros.
+__device__ __forceinline__ uint32_t gather_bytes(const uint32_t u[4], uint32_t sel) {
+    return __builtin_amdgcn_perm(u[1], u[0], sel) | __builtin_amdgcn_perm(u[3], u[2], sel) << 16;
 }
 
-template <int N>
-__device__ __forceinline__ void digits4(const uint32_t u[4], int word, v4i out[N]) {
-    // u: biased values (128 added to every digit but the top one): byte i is digit i plus its bias
-    out[0][word] = (int)(gather_bytes<0>(u[0], u[1], u[2], u[3]) ^ (N > 1 ? 0x80808080u : 0u));
-    if constexpr (N > 1) out[1][word] = (int)(gather_bytes<1>(u[0], u[1], u[2], u[3]) ^ (N > 2 ? 0x80808080u : 0u));
-    if constexpr (N > 2) out[2][word] = (int)(gather_bytes<2>(u[0], u[1], u[2], u[3]) ^ (N > 3 ? 0x80808080u : 0u));
-    if constexpr (N > 3) out[3][word] = (int)gather_bytes<3>(u[0], u[1], u[2], u[3]);
+// v + the value that DPP control CTRL brings.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
+// The sum over a quad of lanes, the same bits in each.
+__device__ __forceinline__ float quad_sum(float v) { return dpp_add<0x4E>(dpp_add<0xB1>(v)); }
 
-// Digit sums (digit 0 lowest) as one fp32 value.
-template <int N>
-__device__ __forceinline__ float join(const int d[N]) {
-    if constexpr (N == 2) return (float)((d[1] << 8) + d[0]);
-    if constexpr (N == 3) return __builtin_fmaf((float)((d[2] << 8) + d[1]), 256.0f, (float)d[0]);
-    return __builtin_fmaf((float)((d[3] << 8) + d[2]), 65536.0f, (float)((d[1] << 8) + d[0]));
-}
-
-template <typename T>
-__device__ __forceinline__ void store_one(T *p, float v) {
-    if constexpr (sizeof(T) == 2)
-        *p = (T)bf16_pair(v, 0.0f);
+__device__ __forceinline__ void store_out(const DecodeArgs &p, int64_t i, float v) {
+    if (p.out_bf16)
+        static_cast<uint16_t *>(p.out)[i] = (uint16_t)bf16_pair(v, 0.0f);
     else
-        *p = v;
+        static_cast<float *>(p.out)[i] = v;
 }
 
-// QD digits of q (3 for bf16, 4 for fp32), PD digits of the weights (2 for a bf16 output, 3 for fp32).
-template <int D, typename QT, typename OT>
-__global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(DecodeArgs p) {
-    constexpr int QD = sizeof(QT) == 2 ? 3 : 4;
-    constexpr int PD = sizeof(OT) == 2 ? 2 : 3;
+template <bool STREAM>
+__device__ __forceinline__ v4i load16(const int8_t *p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const v4i *>(p));
+    return *reinterpret_cast<const v4i *>(p);
+}
+
+// NB blocks of 4 query heads of one key head share each tile's keys and values.
+template <int D, int NB, bool STREAM>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs p) {
     constexpr int kSteps = D / 64;
     constexpr int kDTiles = D / 16;
+    constexpr int kHeads = 4 * NB;
     constexpr int kRow = D + 4;
-    // largest weight of a tile in units of the lowest digit, and the bias of the lower digits
-    constexpr float kUnit = PD == 2 ? 127.0f * 256.0f : 127.0f * 65536.0f;
-    constexpr float kMagic = 8388608.0f + (PD == 2 ? 128.0f : 32896.0f);
+    constexpr float kUnit = 127.0f * 65536.0f;             // a tile's largest weight in units of its lowest digit
+    constexpr float kMagic = 8388608.0f + 128.0f * 257.0f;  // 2^23 and a bias of 128 on the two lower digits
 
-    __shared__ float s_o[kWaves][kCols][kRow];
-    __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
+    __shared__ __align__(16) float s_o[kWaves][kHeads][kRow];
+    __shared__ float s_m[kWaves][kHeads], s_l[kWaves][kHeads];
 
     const int b = blockIdx.z, split = blockIdx.x;
-    const int chunks = (p.group + kCols - 1) / kCols;
-    const int h = blockIdx.y / chunks, first = blockIdx.y % chunks * kCols;
-    const int cols = p.group - first < kCols ? p.group - first : kCols;
+    const int chunks = (p.group + kHeads - 1) / kHeads;
+    const int h = blockIdx.y / chunks, first = blockIdx.y % chunks * kHeads;
+    const int heads = p.group - first < kHeads ? p.group - first : kHeads;
     const int head0 = h * p.group + first;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int c = lane & 15, g = lane >> 4;
+    const int c = lane & 15, g = lane >> 4, dg = c & 3;
 
     int len = p.lengths[b];
     len = len < p.max_len ? len : p.max_len;
@@ -120,180 +123,222 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(DecodeArgs p) 
     const int t1 = t0 + p.chunk < tiles ? t0 + p.chunk : tiles;
     if (split > 0 && t0 >= tiles) return;
 
-    // the query rows' digits: lane (g, c) holds channels 64s + 16g .. +15 of row c
-    v4i qd[kSteps][QD];
-    float qunit;  // value of a unit of the lowest digit, with the softmax scale
-    {
+    const int64_t head_bytes = (int64_t)p.page * D;
+    const int32_t *table = p.table + (int64_t)b * p.slots;
+    const int last_slot = (len - 1) >> p.page_shift;
+
+    // Keys: this lane's rows belong to the tile's 16 tokens number c / 4; its values and scores to number g.
+    // Loads return in the order in which they were issued, so everything is asked for ahead of what is waited on
+    // first: the page numbers two tiles ahead, the next tile's scales and keys as soon as this one's keys are
+    // used up, this tile's values before its scores are computed.
+    struct Pages { int k, v; };
+    const auto pages_of = [&](int t) {
+        int kslot = (t * kTile + 16 * (c >> 2)) >> p.page_shift, vslot = (t * kTile + 16 * g) >> p.page_shift;
+        kslot = kslot < last_slot ? kslot : last_slot;  // pieces past the end read the last page and are masked
+        vslot = vslot < last_slot ? vslot : last_slot;
+        return Pages{table[kslot], table[vslot]};
+    };
+    const auto exists = [&](int page) { return (uint32_t)page < (uint64_t)p.pages; };
+    const auto head_of = [&](int page) { return (int64_t)(exists(page) ? page : 0) * p.kv_heads + h; };
+    v4i kf[4][kSteps];
+    float sk, sv;
+    const auto load_keys = [&](int t, Pages pg) {
+        sk = p.k_scale[head_of(pg.v)];
+        sv = p.v_scale[head_of(pg.v)];
+        const int8_t *kb = p.k + head_of(pg.k) * head_bytes +
+                           (((t * kTile + 16 * (c >> 2)) & (p.page - 1)) + (c & 3)) * D + 16 * g;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) kf[tt][s] = load16<STREAM>(kb + 4 * tt * D + 64 * s);
+    };
+    Pages now{0, 0}, next{0, 0};
+    const bool work = t0 + wave < t1;
+    if (work) {
+        now = pages_of(t0 + wave);
+        next = pages_of(t0 + wave + kWaves);
+    }
+
+    // Query digits: lane (g, c) holds digit dg of channels 64s + 16g .. +15 of head c / 4 of each block.
+    v4i qd[NB][kSteps];
+    float qunit[NB];  // what a unit of this lane's digit is worth in a score, in powers of two
+    const uint32_t qsel = 0x0C0C0000u | (uint32_t)(4 + dg) << 8 | (uint32_t)dg, qflip = dg < 3 ? 0x80808080u : 0u;
+    const float weight = __uint_as_float((uint32_t)(127 + 8 * dg) << 23);  // 256^dg
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
         float f[kSteps][16];
         float most = 0.0f;
-        const bool there = c < cols;
-        const QT *q = static_cast<const QT *>(p.q) + b * p.q_stride + (int64_t)(head0 + (there ? c : 0)) * D + 16 * g;
+        const int head = 4 * n + (c >> 2);
+        const bool there = head < heads;
+        const int64_t at = b * p.q_stride + (int64_t)(head0 + (there ? head : 0)) * D + 16 * g;
+        const auto load_row = [&](const auto *q) {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            load8(q + 64 * s, f[s]);
-            load8(q + 64 * s + 8, f[s] + 8);
+            for (int s = 0; s < kSteps; ++s) {
+                load8(q + 64 * s, f[s]);
+                load8(q + 64 * s + 8, f[s] + 8);
+            }
+        };
+        if (p.q_bf16)
+            load_row(static_cast<const uint16_t *>(p.q) + at);
+        else
+            load_row(static_cast<const float *>(p.q) + at);
+        if (n == 0 && work) load_keys(t0 + wave, now);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 f[s][e] = there ? f[s][e] : 0.0f;
                 most = fmaxf(most, fabsf(f[s][e]));
             }
-        }
         most = max_halves(max_rows16(most));
         int ex;
-        (void)frexpf(most, &ex);  // most < 2^ex, so |value| <= 2^(8 QD - 2)
-        const int up = 8 * QD - 2 - ex;
-        qunit = ldexpf(p.scale2, -up);
-        constexpr uint32_t bias = QD == 3 ? 0x8080u : 0x808080u;
+        (void)frexpf(most, &ex);  // most < 2^ex, so |value| <= 2^30 and its top digit is within +-64
+        qunit[n] = ldexpf(p.scale2 * weight, ex - 30);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 uint32_t u[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) u[e] = (uint32_t)(int)__builtin_rintf(ldexpf(f[s][4 * w + e], up)) + bias;
-                digits4<QD>(u, w, qd[s]);
+                for (int e = 0; e < 4; ++e)
+                    u[e] = (uint32_t)(int)__builtin_rintf(ldexpf(f[s][4 * w + e], 30 - ex)) + 0x808080u;
+                qd[n][s][w] = (int)(gather_bytes(u, qsel) ^ qflip);
             }
     }
+    const uint32_t psel = dg < 3 ? qsel : 0x0C0C0C0Cu, pflip = dg < 2 ? 0x80808080u : 0u;
 
-    float o[kDTiles][4];
+    float o[NB][kDTiles][4];
+    float m[NB], l[NB];  // l: the share of this lane's tokens
 #pragma unroll
-    for (int i = 0; i < kDTiles; ++i)
+    for (int n = 0; n < NB; ++n) {
+        m[n] = -INFINITY;
+        l[n] = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[i][r] = 0.0f;
-    float m = -INFINITY, l = 0.0f;  // l: this lane's share
-
-    const int64_t head_bytes = (int64_t)p.page * D;
-    const int32_t *table = p.table + (int64_t)b * p.slots;
-    const int last_slot = (len - 1) >> p.page_shift;
+        for (int i = 0; i < kDTiles; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[n][i][r] = 0.0f;
+    }
 
     for (int t = t0 + wave; t < t1; t += kWaves) {
-        // keys: this lane's rows belong to the tile's 16 tokens number c / 4, its values to number g
-        const int kt = t * kTile + 16 * (c >> 2), vt = t * kTile + 16 * g;
-        int kslot = kt >> p.page_shift, vslot = vt >> p.page_shift;
-        kslot = kslot < last_slot ? kslot : last_slot;  // pieces past the end read the last page and are masked
-        vslot = vslot < last_slot ? vslot : last_slot;
-        int kp = table[kslot], vp = table[vslot];
-        const bool kvalid = (uint32_t)kp < (uint64_t)p.pages, vvalid = (uint32_t)vp < (uint64_t)p.pages;
-        kp = kvalid ? kp : 0;
-        vp = vvalid ? vp : 0;
-        const int8_t *kb = p.k + ((int64_t)kp * p.kv_heads + h) * head_bytes +
-                           ((kt & (p.page - 1)) + (c & 3)) * D + 16 * g;
-        const int64_t vhead = (int64_t)vp * p.kv_heads + h;
-        const int8_t *vb = p.v + vhead * head_bytes + c * p.page + (vt & (p.page - 1));
-        const float sk = p.k_scale[vhead] * qunit, sv = p.v_scale[vhead];
+        const int vt = t * kTile + 16 * g;
+        const bool vvalid = exists(now.v);
+        const int8_t *vb = p.v + head_of(now.v) * head_bytes + c * p.page + (vt & (p.page - 1));
+        const float sk_t = sk, sv_t = sv;
+        v4i vf[kDTiles];
+#pragma unroll
+        for (int i = 0; i < kDTiles; ++i) vf[i] = load16<STREAM>(vb + 16 * i * p.page);
+        const Pages after = pages_of(t + 2 * kWaves);
+        __builtin_amdgcn_sched_barrier(0);  // or the compiler moves these loads behind the scores, to spare registers
 
-        v4i kf[4][kSteps], vf[kDTiles];
+        v4i score[NB][4];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) kf[tt][s] = *reinterpret_cast<const v4i *>(kb + 4 * tt * D + 64 * s);
+            for (int tt = 0; tt < 4; ++tt) {
+                score[n][tt] = v4i{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < kDTiles; ++i) vf[i] = *reinterpret_cast<const v4i *>(vb + 16 * i * p.page);
+                for (int st = 0; st < kSteps; ++st) score[n][tt] = mfma_i8(kf[tt][st], qd[n][st], score[n][tt]);
+            }
+        // without a branch, so that the waits below count the loads; behind the last tile that tile once more, from L2
+        load_keys(t + kWaves < t1 ? t + kWaves : t, t + kWaves < t1 ? next : now);
+        __builtin_amdgcn_sched_barrier(0);
+        now = next;
+        next = after;
 
-        float s[16];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-            v4i acc[QD];
-#pragma unroll
-            for (int d = 0; d < QD; ++d) {
-                acc[d] = v4i{0, 0, 0, 0};
-#pragma unroll
-                for (int st = 0; st < kSteps; ++st) acc[d] = mfma_i8(kf[tt][st], qd[st][d], acc[d]);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                int d[QD];
-#pragma unroll
-                for (int i = 0; i < QD; ++i) d[i] = acc[i][r];
-                s[4 * tt + r] = join<QD>(d) * sk;
-            }
-        }
         const int seen = vvalid ? len - vt : 0;  // of this lane's 16 tokens (may exceed 16 or be negative)
-        if (seen < 16) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = i < seen ? s[i] : -INFINITY;
-        }
-        float mt = s[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mt = fmaxf(mt, s[i]);
-        mt = max_halves(max_rows16(mt));
-        const float ref = mt == -INFINITY ? 0.0f : mt;  // a tile of which nothing is seen: all weights 0
         // scales of the four 16-token groups, under the largest
-        const float svs = seen > 0 ? sv : 0.0f;
+        const float svs = seen > 0 ? sv_t : 0.0f;
         const float svmax = max_halves(max_rows16(svs));
         const float ratio = svmax > 0.0f ? svs / svmax * kUnit : 0.0f;
-
-        float sum = 0.0f;
-        v4i pd[PD];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            uint32_t u[4];
+        for (int n = 0; n < NB; ++n) {
+            const float unit = sk_t * qunit[n];
+            float s[16];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float e = __builtin_amdgcn_exp2f(s[4 * w + r] - ref);
-                sum += e;
-                // one fused product and sum rounds to a whole number in the low bits of the mantissa
-                u[r] = __float_as_uint(__builtin_fmaf(e, ratio, kMagic));
+            for (int i = 0; i < 16; ++i) s[i] = quad_sum((float)score[n][i / 4][i % 4] * unit);
+            if (seen < 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = i < seen ? s[i] : -INFINITY;
             }
-            digits4<PD>(u, w, pd);
-        }
+            float mt = s[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) mt = fmaxf(mt, s[i]);
+            mt = max_halves(max_rows16(mt));
+            const float ref = mt == -INFINITY ? 0.0f : mt;  // a tile of which nothing is seen: all weights 0
 
-        const float mn = fmaxf(m, mt);
-        const float mref = mn == -INFINITY ? 0.0f : mn;
-        const float beta = __builtin_amdgcn_exp2f(mt - mref);
-        if (__any(mn > m)) {
-            const float alpha = __builtin_amdgcn_exp2f(m - mref);
-            l *= alpha;
+            float sum = 0.0f;
+            v4i pd;
 #pragma unroll
-            for (int i = 0; i < kDTiles; ++i)
+            for (int w = 0; w < 4; ++w) {
+                uint32_t u[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) o[i][r] *= alpha;
+                for (int r = 0; r < 4; ++r) {
+                    const float e = __builtin_amdgcn_exp2f(s[4 * w + r] - ref);
+                    sum += e;
+                    // one fused product and sum rounds to a whole number in the low bits of the mantissa
+                    u[r] = __float_as_uint(__builtin_fmaf(e, ratio, kMagic));
+                }
+                pd[w] = (int)(gather_bytes(u, psel) ^ pflip);
+            }
+
+            const float mn = fmaxf(m[n], mt);
+            const float mref = mn == -INFINITY ? 0.0f : mn;
+            const float beta = __builtin_amdgcn_exp2f(mt - mref);
+            if (__any(mn > m[n])) {
+                const float alpha = __builtin_amdgcn_exp2f(m[n] - mref);
+                l[n] *= alpha;
+#pragma unroll
+                for (int i = 0; i < kDTiles; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[n][i][r] *= alpha;
+            }
+            m[n] = mn;
+            l[n] = __builtin_fmaf(sum, beta, l[n]);
+            const float w = beta * svmax * weight * (1.0f / kUnit);
+#pragma unroll
+            for (int i = 0; i < kDTiles; ++i) {
+                const v4i acc = mfma_i8(vf[i], pd, v4i{0, 0, 0, 0});
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[n][i][r] = __builtin_fmaf((float)acc[r], w, o[n][i][r]);
+            }
+            if constexpr (NB > 1) __builtin_amdgcn_sched_barrier(0);  // one block's weights at a time, for the registers
         }
-        m = mn;
-        l = __builtin_fmaf(sum, beta, l);
-        const float w = beta * svmax * (1.0f / kUnit);
+    }
+
+    // join the digits, then the waves
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const int head = 4 * n + (c >> 2);
+        const float ls = add_halves(add_rows16(l[n]));
+        if (g == 0 && dg == 0) {
+            s_m[wave][head] = m[n];
+            s_l[wave][head] = ls;
+        }
 #pragma unroll
         for (int i = 0; i < kDTiles; ++i) {
-            v4i acc[PD];
+            v4f x;
 #pragma unroll
-            for (int d = 0; d < PD; ++d) acc[d] = mfma_i8(vf[i], pd[d], v4i{0, 0, 0, 0});
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                int d[PD];
-#pragma unroll
-                for (int x = 0; x < PD; ++x) d[x] = acc[x][r];
-                o[i][r] = __builtin_fmaf(join<PD>(d), w, o[i][r]);
-            }
+            for (int r = 0; r < 4; ++r) x[r] = quad_sum(o[n][i][r]);
+            if ((i & 3) == dg) *reinterpret_cast<v4f *>(&s_o[wave][head][16 * i + 4 * g]) = x;
         }
     }
-
-    // join the waves
-    l = add_halves(add_rows16(l));
-    if (g == 0) {
-        s_m[wave][c] = m;
-        s_l[wave][c] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < kDTiles; ++i)
-        *reinterpret_cast<v4f *>(&s_o[wave][c][16 * i + 4 * g]) = v4f{o[i][0], o[i][1], o[i][2], o[i][3]};
     __syncthreads();
-    for (int i = tid; i < cols * D; i += 64 * kWaves) {
+    for (int i = tid; i < heads * D; i += 64 * kWaves) {
         const int col = i / D, d = i % D;
         float mm = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, s_m[w][col]);
+        const float ref = mm == -INFINITY ? 0.0f : mm;
         float ll = 0.0f, oo = 0.0f;
-        if (mm != -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float a = __builtin_amdgcn_exp2f(s_m[w][col] - mm);
-                ll = __builtin_fmaf(a, s_l[w][col], ll);
-                oo = __builtin_fmaf(a, s_o[w][col][d], oo);
-            }
+        for (int w = 0; w < kWaves; ++w) {
+            const float a = __builtin_amdgcn_exp2f(s_m[w][col] - ref);
+            ll = __builtin_fmaf(a, s_l[w][col], ll);
+            oo = __builtin_fmaf(a, s_o[w][col][d], oo);
         }
         const int64_t row = (int64_t)b * p.q_heads + head0 + col;
         if (p.splits == 1) {
-            store_one(static_cast<OT *>(p.out) + row * D + d, ll > 0.0f ? oo / ll : 0.0f);
+            store_out(p, row * D + d, ll > 0.0f ? oo / ll : 0.0f);
         } else {
             p.part[(row * p.splits + split) * D + d] = oo;
             if (d == 0) {
@@ -305,10 +350,14 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(DecodeArgs p) 
     }
 }
 
-// Joins the splits of one query row.
-template <int D, typename OT>
-__global__ __launch_bounds__(D) void attn_join_kernel(DecodeArgs p) {
-    const int b = blockIdx.y, d = threadIdx.x;
+// Joins the splits of one query row: 8 runs of splits side by side, 4 channels a lane.
+constexpr int kJoinRuns = 8;
+template <int D>
+__global__ __launch_bounds__(kJoinRuns *D / 4) void attn_join_kernel(DecodeArgs p) {
+    __shared__ __align__(16) float s_o[kJoinRuns][D];
+    __shared__ float s_l[kJoinRuns];
+    const int b = blockIdx.y, tid = threadIdx.x;
+    const int run = tid / (D / 4), d = tid % (D / 4) * 4;
     const int64_t row = (int64_t)b * p.q_heads + blockIdx.x;
     int len = p.lengths[b];
     len = len < p.max_len ? len : p.max_len;
@@ -316,45 +365,69 @@ __global__ __launch_bounds__(D) void attn_join_kernel(DecodeArgs p) {
     if (len > room) len = (int)room;
     const int tiles = len > 0 ? (len + kTile - 1) / kTile : 0;
     const int n = tiles > p.chunk ? (tiles + p.chunk - 1) / p.chunk : 1;  // the split 0 is always written
-    const float *stat = p.part + (int64_t)gridDim.y * p.q_heads * p.splits * D + row * p.splits * 2;
+    const float2 *stat = reinterpret_cast<const float2 *>(p.part + (int64_t)gridDim.y * p.q_heads * p.splits * D) +
+                         row * p.splits;
     const float *part = p.part + row * p.splits * D + d;
-    float mm = -INFINITY;
-    for (int i = 0; i < n; ++i) mm = fmaxf(mm, stat[2 * i]);
-    float ll = 0.0f, oo = 0.0f;
-    if (mm != -INFINITY)
-        for (int i = 0; i < n; ++i) {
-            const float a = __builtin_amdgcn_exp2f(stat[2 * i] - mm);
-            ll = __builtin_fmaf(a, stat[2 * i + 1], ll);
-            oo = __builtin_fmaf(a, part[(int64_t)i * D], oo);
+    float mm = -INFINITY;  // every wave for itself
+    for (int i = tid & 63; i < n; i += 64) mm = fmaxf(mm, stat[i].x);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+    float ll = 0.0f;
+    v4f oo = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = run; i < n; i += kJoinRuns) {
+        const float2 st = stat[i];
+        const v4f x = *reinterpret_cast<const v4f *>(part + (int64_t)i * D);
+        const float a = __builtin_amdgcn_exp2f(st.x - ref);
+        ll = __builtin_fmaf(a, st.y, ll);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oo[e] = __builtin_fmaf(a, x[e], oo[e]);
+    }
+    *reinterpret_cast<v4f *>(&s_o[run][d]) = oo;
+    if (d == 0) s_l[run] = ll;
+    __syncthreads();
+    for (int i = tid; i < D; i += kJoinRuns * D / 4) {
+        float sum = 0.0f, w = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kJoinRuns; ++r) {
+            sum += s_o[r][i];
+            w += s_l[r];
         }
-    store_one(static_cast<OT *>(p.out) + row * D + d, ll > 0.0f ? oo / ll : 0.0f);
+        store_out(p, row * D + i, w > 0.0f ? sum / w : 0.0f);
+    }
 }
 
-// Tiles of one workgroup: enough workgroups to fill the chip, at least one tile for each wave.
+// Query heads of one workgroup, in blocks of 4: more than 8 do not fit the registers, and larger groups read
+// their keys and values once for every 8.
+int heads_of(int group) { return group <= 4 ? 4 : 8; }
+
+// Tiles of one workgroup.  The longest contexts are cut so that all workgroups are resident at once
+// (one more than that would double the time), but no finer than a tile for each wave.
 int chunk_of(int batch, int kv_heads, int group, int tiles) {
-    const int64_t rows = (int64_t)batch * kv_heads * ((group + kCols - 1) / kCols);
-    int64_t splits = (kWantGroups + rows - 1) / rows;
-    int64_t chunk = (tiles + splits - 1) / splits;
+    const int heads = heads_of(group);
+    const int64_t rows = (int64_t)batch * kv_heads * ((group + heads - 1) / heads);
+    const int64_t splits = rows < kWantGroups ? kWantGroups / rows : 1;
+    const int64_t chunk = (tiles + splits - 1) / splits;
     return chunk < kWaves ? kWaves : (int)chunk;
 }
 
-template <int D, typename QT, typename OT>
-void launch_decode(const DecodeArgs &p, int batch, hipStream_t stream) {
-    const int chunks = (p.group + kCols - 1) / kCols;
-    hipLaunchKernelGGL((attn_decode_kernel<D, QT, OT>), dim3(p.splits, p.kv_heads * chunks, batch), dim3(64 * kWaves), 0,
-                       stream, p);
-    if (p.splits > 1)
-        hipLaunchKernelGGL((attn_join_kernel<D, OT>), dim3(p.q_heads, batch), dim3(D), 0, stream, p);
+template <int D, int NB>
+void launch_decode(const DecodeArgs &p, dim3 grid, hipStream_t stream) {
+    const int64_t bytes = 2ll * grid.z * p.kv_heads * p.max_len * D;
+    if (p.page <= 64 && bytes > kStreamBytes)
+        hipLaunchKernelGGL((attn_decode_kernel<D, NB, true>), grid, dim3(64 * kWaves), 0, stream, p);
+    else
+        hipLaunchKernelGGL((attn_decode_kernel<D, NB, false>), grid, dim3(64 * kWaves), 0, stream, p);
 }
 
 template <int D>
-void launch_types(const DecodeArgs &p, int qdt, int odt, int batch, hipStream_t stream) {
-    if (qdt == BITNET_DT_BF16)
-        odt == BITNET_DT_BF16 ? launch_decode<D, uint16_t, uint16_t>(p, batch, stream)
-                              : launch_decode<D, uint16_t, float>(p, batch, stream);
-    else
-        odt == BITNET_DT_BF16 ? launch_decode<D, float, uint16_t>(p, batch, stream)
-                              : launch_decode<D, float, float>(p, batch, stream);
+void launch(const DecodeArgs &p, int batch, hipStream_t stream) {
+    const int heads = heads_of(p.group);
+    const dim3 grid(p.splits, p.kv_heads * ((p.group + heads - 1) / heads), batch);
+    heads == 4 ? launch_decode<D, 1>(p, grid, stream) : launch_decode<D, 2>(p, grid, stream);
+    if (p.splits > 1)
+        hipLaunchKernelGGL((attn_join_kernel<D>), dim3(p.q_heads, batch), dim3(kJoinRuns * D / 4), 0, stream, p);
 }
 
 bool decode_shape_ok(int batch, int q_heads, int kv_heads, int head_dim, int max_len) {
@@ -402,7 +475,9 @@ bitnet_status_t bitnet_attn_decode(const void *q, int qdt, int64_t q_stride, con
     p.page = cache->page; p.page_shift = __builtin_ctz((unsigned)cache->page); p.slots = cache->slots; p.max_len = max_len;
     p.scale2 = scale * 1.44269504088896340736f;
     p.out = out; p.part = static_cast<float *>(workspace);
-    D == 64 ? launch_types<64>(p, qdt, odt, cache->batch, stream) : launch_types<128>(p, qdt, odt, cache->batch, stream);
+    p.q_bf16 = qdt == BITNET_DT_BF16;
+    p.out_bf16 = odt == BITNET_DT_BF16;
+    D == 64 ? launch<64>(p, cache->batch, stream) : launch<128>(p, cache->batch, stream);
     return launched();
 }
 
