@@ -561,32 +561,72 @@ def bitnet_rope_table(positions: int, rot: int, base: float = 10000.0, factor: f
 
 
 def _cache_struct(k_cache, v_cache, k_scale, v_scale, table):
-    """bitnet_kv_cache_t over the given tensors, each checked against the layout of the header."""
+    """(bitnet_kv_cache_t over the given tensors, their device index), each tensor checked against the layout of the
+    header.  One combined test first: a serving step makes this call for every layer."""
     import torch
+    i8, f32 = torch.int8, torch.float32
+    dev = k_cache.get_device()
+    if k_cache.dim() == 4 and table.dim() == 2:
+        pages, heads, page, dim = k_cache.shape
+        batch, slots = table.shape
+        if (k_cache.dtype is i8 and v_cache.dtype is i8 and k_scale.dtype is f32 and v_scale.dtype is f32
+                and table.dtype is torch.int32 and v_cache.shape == (pages, heads, dim, page)
+                and k_scale.shape == (pages, heads) and v_scale.shape == (pages, heads) and dev >= 0
+                and dev == v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == table.get_device()
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous() and table.is_contiguous()):
+            return KVCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                 table.data_ptr(), pages, heads, dim, page, batch, slots), dev
+    # something is wrong: say what
     if k_cache.dim() != 4 or table.dim() != 2:
         raise ValueError("k_cache must be [pages][kv_heads][page][head_dim] and table [batch][slots]")
     pages, heads, page, dim = k_cache.shape
-    _check(k_cache, "k_cache", torch.int8)
-    _check(v_cache, "v_cache", torch.int8, shape=(pages, heads, dim, page))
-    _check(k_scale, "k_scale", torch.float32, shape=(pages, heads))
-    _check(v_scale, "v_scale", torch.float32, shape=(pages, heads))
+    _check(k_cache, "k_cache", i8)
+    _check(v_cache, "v_cache", i8, shape=(pages, heads, dim, page))
+    _check(k_scale, "k_scale", f32, shape=(pages, heads))
+    _check(v_scale, "v_scale", f32, shape=(pages, heads))
     _check(table, "table", torch.int32)
-    return KVCacheStruct(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _dev_ptr(k_scale, "k_scale"),
-                         _dev_ptr(v_scale, "v_scale"), _dev_ptr(table, "table"), pages, heads, dim, page,
-                         table.shape[0], table.shape[1])
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"),
+                    (table, "table")):
+        _on_device(t, name, dev)
+    raise ValueError("the cache's tensors do not fit together")
 
 
-def _rows_ptr(t, name: str, inner: int):
+def _on_device(t, name: str, dev: int, dtype=None, shape=None):
+    """Pointer of a contiguous tensor on device `dev`, of the given dtype and shape where they are named."""
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a device tensor" if t.get_device() < 0 else
+                         f"{name} must be on the device of the other tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if (dtype is not None and t.dtype is not dtype) or (shape is not None and t.shape != shape):
+        _check(t, name, dtype, shape=shape)
+    return t.data_ptr()
+
+
+def _launch_stream(stream, dev: int):
+    """The stream handle of a launch on device `dev`, which has to be the current one."""
+    import torch
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"the tensors are on device {dev}, the current device is {torch.cuda.current_device()}")
+    # the handle alone: current_stream() builds an object around it, for as long as a launch takes
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _rows_ptr(t, name: str, inner: int, dev: int):
     """(pointer, elements from row to row) of a device tensor whose rows hold `inner` elements side by side:
     contiguous, or a slice of wider rows."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a device tensor" if t.get_device() < 0 else
+                         f"{name} must be on the device of the other tensors")
+    if t.is_contiguous():
+        return t.data_ptr(), inner
     want = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != want:
             raise ValueError(f"{name} must have its heads and channels side by side in a row")
         want *= size
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else inner
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else inner
 
 
 def _empty(shape, dtype, device, stream):
@@ -601,10 +641,11 @@ def _empty(shape, dtype, device, stream):
 
 def _float_dt(t, name: str) -> int:
     import torch
-    dt = {torch.bfloat16: BITNET_DT_BF16, torch.float32: BITNET_DT_F32}.get(t.dtype if hasattr(t, "dtype") else t)
-    if dt is None:
-        raise ValueError(f"{name} must be bf16 or fp32")
-    return dt
+    if t.dtype is torch.bfloat16:
+        return BITNET_DT_BF16
+    if t.dtype is torch.float32:
+        return BITNET_DT_F32
+    raise ValueError(f"{name} must be bf16 or fp32")
 
 
 def bitnet_rope_append_kv(qkv, rope, k_cache, v_cache, k_scale, v_scale, table, starts, before, max_new: int,
@@ -615,35 +656,35 @@ def bitnet_rope_append_kv(qkv, rope, k_cache, v_cache, k_scale, v_scale, table, 
     None; starts int32 [batch + 1], before int32 [batch].  Returns (q [T][q_heads][head_dim], k or None); k,
     the turned keys, is made when with_k or k_out asks for it."""
     import torch
-    c = _cache_struct(k_cache, v_cache, k_scale, v_scale, table)
+    c, dev = _cache_struct(k_cache, v_cache, k_scale, v_scale, table)
     dt = _float_dt(qkv, "qkv")
-    width = (q_heads + 2 * c.kv_heads) * c.head_dim
+    hk, dim, batch = c.kv_heads, c.head_dim, c.batch
+    width = (q_heads + 2 * hk) * dim
     if qkv.dim() != 2 or qkv.shape[1] != width:
         raise ValueError(f"qkv must be [T][{width}], not {tuple(qkv.shape)}")
     T = qkv.shape[0]
-    _check(starts, "starts", torch.int32, shape=(c.batch + 1,))
-    _check(before, "before", torch.int32, shape=(c.batch,))
+    sp = _on_device(starts, "starts", dev, torch.int32, (batch + 1,))
+    bp = _on_device(before, "before", dev, torch.int32, (batch,))
     rot = rows = 0
     rp = None
     if rope is not None:
-        _check(rope, "rope", torch.float32)
         if rope.dim() != 2:
             raise ValueError("rope must be [positions][rot]")
+        rp = _on_device(rope, "rope", dev, torch.float32)
         rows, rot = rope.shape
-        rp = _dev_ptr(rope, "rope")
-    xp, stride = _rows_ptr(qkv, "qkv", width)
+    xp, stride = _rows_ptr(qkv, "qkv", width, dev)
     if q_out is None:
-        q_out = _empty((T, q_heads, c.head_dim), qkv.dtype, qkv.device, stream)
-    if k_out is None and with_k:
-        k_out = _empty((T, c.kv_heads, c.head_dim), qkv.dtype, qkv.device, stream)
-    _check(q_out, "q_out", qkv.dtype, numel=T * q_heads * c.head_dim)
-    kp = None
+        q_out = _empty((T, q_heads, dim), qkv.dtype, qkv.device, stream)
+    else:
+        _check(q_out, "q_out", qkv.dtype, numel=T * q_heads * dim)
     if k_out is not None:
-        _check(k_out, "k_out", qkv.dtype, numel=T * c.kv_heads * c.head_dim)
-        kp = _dev_ptr(k_out, "k_out")
-    _ok(lib().bitnet_rope_append_kv(xp, dt, stride, rp, rows, rot, int(bool(interleaved)), _dev_ptr(starts, "starts"),
-                                    _dev_ptr(before, "before"), T, int(max_new), int(q_heads), ctypes.byref(c),
-                                    _dev_ptr(q_out, "q_out"), kp, _stream(stream)), "bitnet_rope_append_kv")
+        _check(k_out, "k_out", qkv.dtype, numel=T * hk * dim)
+    elif with_k:
+        k_out = _empty((T, hk, dim), qkv.dtype, qkv.device, stream)
+    _ok(lib().bitnet_rope_append_kv(xp, dt, stride, rp, rows, rot, bool(interleaved), sp, bp, T, max_new, q_heads,
+                                    ctypes.byref(c), _on_device(q_out, "q_out", dev),
+                                    None if k_out is None else _on_device(k_out, "k_out", dev),
+                                    _launch_stream(stream, dev)), "bitnet_rope_append_kv")
     return q_out, k_out
 
 
@@ -658,29 +699,30 @@ def bitnet_attn_decode(q, k_cache, v_cache, k_scale, v_scale, table, lengths, ma
     int32 [batch] counts the cached tokens, max_len bounds them.  scale defaults to 1/sqrt(head_dim).  Returns
     [batch][q_heads][head_dim] in out_dtype (q's by default).  The workspace is allocated unless given."""
     import torch
-    c = _cache_struct(k_cache, v_cache, k_scale, v_scale, table)
+    c, dev = _cache_struct(k_cache, v_cache, k_scale, v_scale, table)
     qdt = _float_dt(q, "q")
-    if q.dim() != 3 or q.shape[0] != c.batch or q.shape[2] != c.head_dim:
-        raise ValueError(f"q must be [{c.batch}][q_heads][{c.head_dim}], not {tuple(q.shape)}")
+    batch, dim = c.batch, c.head_dim
+    if q.dim() != 3 or q.shape[0] != batch or q.shape[2] != dim:
+        raise ValueError(f"q must be [{batch}][q_heads][{dim}], not {tuple(q.shape)}")
     hq = q.shape[1]
-    _check(lengths, "lengths", torch.int32, shape=(c.batch,))
+    qp, stride = _rows_ptr(q, "q", hq * dim, dev)
+    lp = _on_device(lengths, "lengths", dev, torch.int32, (batch,))
     if out is None:
-        out = _empty((c.batch, hq, c.head_dim), out_dtype or q.dtype, q.device, stream)
+        out = _empty((batch, hq, dim), out_dtype or q.dtype, q.device, stream)
+    else:
+        _check(out, "out", out_dtype or out.dtype, numel=batch * hq * dim)
     odt = _float_dt(out, "out")
-    _check(out, "out", out_dtype or out.dtype, numel=c.batch * hq * c.head_dim)
-    need = lib().bitnet_attn_decode_workspace_bytes(c.batch, hq, c.kv_heads, c.head_dim, int(max_len))
-    wp, nb = None, 0
+    need = lib().bitnet_attn_decode_workspace_bytes(batch, hq, c.kv_heads, dim, max_len)
     if workspace is None and need:
         workspace = _empty((need,), torch.uint8, q.device, stream)
+    wp, nb = None, 0
     if workspace is not None:
-        _check(workspace, "workspace", torch.uint8)
-        wp, nb = _dev_ptr(workspace, "workspace"), workspace.numel()
+        wp, nb = _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel()
         if nb < need:
             raise ValueError(f"workspace must hold at least {need} bytes")
-    qp, stride = _rows_ptr(q, "q", hq * c.head_dim)
-    _ok(lib().bitnet_attn_decode(qp, qdt, stride, ctypes.byref(c), _dev_ptr(lengths, "lengths"), int(max_len), hq,
-                                 c.head_dim ** -0.5 if scale is None else float(scale), _dev_ptr(out, "out"), odt, wp, nb,
-                                 _stream(stream)), "bitnet_attn_decode")
+    _ok(lib().bitnet_attn_decode(qp, qdt, stride, ctypes.byref(c), lp, max_len, hq,
+                                 dim ** -0.5 if scale is None else scale, _on_device(out, "out", dev), odt, wp, nb,
+                                 _launch_stream(stream, dev)), "bitnet_attn_decode")
     return out
 
 
@@ -692,23 +734,25 @@ def bitnet_attn_prompt(q, k, v, starts, max_len: int, causal: bool = True, scale
     import torch
     if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or v.shape != k.shape:
         raise ValueError("q must be [T][q_heads][head_dim], k and v [T][kv_heads][head_dim]")
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _check(t, name, torch.bfloat16)
-    _check(starts, "starts", torch.int32)
+    bf16 = torch.bfloat16
+    if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16:
+        raise ValueError("q, k and v must be bf16")
     if starts.dim() != 1 or starts.shape[0] < 2:
         raise ValueError("starts must be [batch + 1]")
     T, hq, dim = q.shape
     hk = k.shape[1]
+    dev = q.get_device()
+    qp, qs = _rows_ptr(q, "q", hq * dim, dev)
+    kp, ks = _rows_ptr(k, "k", hk * dim, dev)
+    vp, vs = _rows_ptr(v, "v", hk * dim, dev)
+    sp = _on_device(starts, "starts", dev, torch.int32)
     if out is None:
-        out = _empty((T, hq, dim), torch.bfloat16, q.device, stream)
-    _check(out, "out", torch.bfloat16, numel=T * hq * dim)
-    qp, qs = _rows_ptr(q, "q", hq * dim)
-    kp, ks = _rows_ptr(k, "k", hk * dim)
-    vp, vs = _rows_ptr(v, "v", hk * dim)
-    _ok(lib().bitnet_attn_prompt(qp, qs, kp, ks, vp, vs, _dev_ptr(starts, "starts"), starts.shape[0] - 1, T,
-                                 int(max_len), hq, hk, dim, int(bool(causal)),
-                                 dim ** -0.5 if scale is None else float(scale), _dev_ptr(out, "out"), _stream(stream)),
-        "bitnet_attn_prompt")
+        out = _empty((T, hq, dim), bf16, q.device, stream)
+    else:
+        _check(out, "out", bf16, numel=T * hq * dim)
+    _ok(lib().bitnet_attn_prompt(qp, qs, kp, ks, vp, vs, sp, starts.shape[0] - 1, T, max_len, hq, hk, dim, bool(causal),
+                                 dim ** -0.5 if scale is None else scale, _on_device(out, "out", dev),
+                                 _launch_stream(stream, dev)), "bitnet_attn_prompt")
     return out
 
 

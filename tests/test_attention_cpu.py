@@ -204,11 +204,14 @@ def test_rows_may_be_slices_of_wider_rows_but_not_strided_inside():
     import torch
 
     class OnDevice(torch.Tensor):
-        is_cuda = True
+        def get_device(self):
+            return 0
     t = torch.zeros(6, 4, 64).as_subclass(OnDevice)
-    assert bn._rows_ptr(t, "t", 256)[1] == 256
-    assert bn._rows_ptr(t[:1], "t", 256)[1] == 256
-    assert bn._rows_ptr(t[:, :2], "t", 128)[1] == 256
+    assert bn._rows_ptr(t, "t", 256, 0)[1] == 256
+    assert bn._rows_ptr(t[:1], "t", 256, 0)[1] == 256
+    assert bn._rows_ptr(t[:, :2], "t", 128, 0)[1] == 256
     for bad in (t[:, ::2], t[:, :, ::2], t.transpose(1, 2)):
         with pytest.raises(ValueError):
-            bn._rows_ptr(bad, "t", 128)
+            bn._rows_ptr(bad, "t", 128, 0)
+    with pytest.raises(ValueError, match="other tensors"):
+        bn._rows_ptr(t, "t", 256, 1)
