@@ -26,11 +26,17 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
+#ifndef OCC64
+#define OCC64 2
+#endif
 constexpr int kWaves = 4;
 constexpr int kRowsWave = 32;                 // query rows of a wave
 constexpr int kRows = kWaves * kRowsWave;     // and of a workgroup
-constexpr int kKeys = 64;                     // keys of a tile
-constexpr int64_t kMaxTokens = 1 << 24;
+constexpr int kKeys = 32;                     // keys of a step
+constexpr int kStages = 4;                    // steps of K and of V in LDS
+constexpr float kSlack = 8.0f;                // log2 of the largest weight before a row's reference moves
+constexpr int64_t kMaxTokens = 1 << 22;  // rows of workgroups of the launch inside 16 bits
+constexpr int64_t kMaxStride = 1 << 23;
 
 struct PromptArgs {
     const uint16_t *q, *k, *v;
@@ -42,160 +48,304 @@ struct PromptArgs {
     uint16_t *out;
 };
 
-// Byte offset of the 16-byte piece `ch` of row `row` in a tile.  Rows are a multiple of the LDS
-// banks apart, so the pieces of a row are permuted by its number: for K a read takes one piece
-// of each of 32 rows; for V, 32 bytes (a pair of pieces) of each of 4 rows.
+// Place of the 16-byte piece `ch` of row `row` in a tile (and, being its own inverse, the piece at a place).
+// Rows are a multiple of the LDS banks apart, so the pieces of a row are permuted by its number: for K a read
+// takes one piece of each of 16 rows at a time; for V, 64 bytes of each of 4 rows.
 template <int D>
-__device__ __forceinline__ int k_at(int row, int ch) {
-    return row * (2 * D) + ((ch ^ (row & (D / 8 - 1))) << 4);
+__device__ __forceinline__ int k_piece(int row, int ch) {
+    return ch ^ (row & (D / 8 - 1));
 }
 template <int D>
-__device__ __forceinline__ int v_at(int row, int ch) {
-    return row * (2 * D) + ((ch ^ ((row & (D / 16 - 1)) << 1)) << 4);
+__device__ __forceinline__ int v_piece(int row, int ch) {
+    return ch ^ (D == 128 ? (row & 3) << 2 : (row & 2) << 1);
 }
 
-template <int D>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs p) {
-    constexpr int kTileBytes = kKeys * D * 2;
-    constexpr int kPieces = kKeys * D / 8 / (64 * kWaves);  // 16-byte pieces of K (and of V) that a thread stages
-    constexpr int kKSteps = D / 16;
-    constexpr int kDTiles = D / 32;
-    __shared__ __align__(16) uint8_t s_k[2][kTileBytes];
-    __shared__ __align__(16) uint8_t s_v[2][kTileBytes];
+// 16 bytes a lane from global memory (base + offset) to LDS at lds + 16 * lane.  M0 carries the LDS address.
+__device__ __forceinline__ void dma16(const void *base, uint32_t offset, uint32_t lds) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %2, %3\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(lds), "v"(offset), "s"(base)
+        : "memory");
+}
 
-    const int b = blockIdx.z, head = blockIdx.y;
+// Waits until at most N of this wave's direct loads are pending, then meets the workgroup.
+template <int N>
+__device__ __forceinline__ void wait_loads_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+#define INLINE __attribute__((always_inline))
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_kernel(PromptArgs p) {
+    constexpr int kRowBytes = 2 * D;
+    constexpr int kTileBytes = kKeys * kRowBytes;
+    constexpr int kK = D / 16;              // products of a step's scores
+    constexpr int kD = D / 32;              // channel tiles of the second product, two products each
+    constexpr int kSlots = kK + 2 * kD;
+    constexpr int kScores = 16 / kSlots;    // weights computed beside a product
+    constexpr int kLoads = kTileBytes / 1024 / kWaves;  // direct loads of a wave for a step of K (or V)
+    __shared__ __align__(1024) uint8_t s_k[kStages][kTileBytes];
+    __shared__ __align__(1024) uint8_t s_v[kStages][kTileBytes];
+
+    const int b = blockIdx.y, head = blockIdx.x;
     const int64_t n0 = p.starts[b], n1 = p.starts[b + 1];
     if (n0 < 0 || n1 > p.tokens || n1 <= n0) return;
     const int n = (int)(n1 - n0 < p.max_len ? n1 - n0 : p.max_len);
-    const int q0 = (int)(gridDim.x - 1 - blockIdx.x) * kRows;  // the longest rows first
+    const int q0 = (int)(gridDim.z - 1 - blockIdx.z) * kRows;  // the longest rows of all heads and sequences first
     if (q0 >= n) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int hk = head / (p.q_heads / p.kv_heads);
     const uint16_t *kg = p.k + n0 * p.k_stride + (int64_t)hk * D;
     const uint16_t *vg = p.v + n0 * p.v_stride + (int64_t)hk * D;
 
     const int w0 = q0 + wave * kRowsWave;  // this wave's first row
-    const int row = w0 + col;              // this lane's query row
-    v8bf qf[kKSteps];
+    const int row = w0 + col;              // this lane's
+    const int seen = p.causal && q0 + kRows < n ? q0 + kRows : n;  // keys that any row of the workgroup sees
+    const int steps = (seen + kKeys - 1) / kKeys;
+    const int wave_seen = w0 >= n ? 0 : p.causal && w0 + kRowsWave < n ? w0 + kRowsWave : n;
+    const int wave_steps = (wave_seen + kKeys - 1) / kKeys;
+    const int whole = (p.causal && w0 + 1 < n ? w0 + 1 : n) / kKeys;  // steps that every row of the wave sees whole
+
+    // ---- direct loads: a lane's places in LDS are fixed, and with them its rows and pieces
+    uint32_t k_off[kLoads], v_off[kLoads];
+    const auto places = [&](int left, uint32_t (&ko)[kLoads], uint32_t (&vo)[kLoads]) INLINE {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int at = (wave * kLoads + i) * 1024 + lane * 16;
+            const int r0 = at / kRowBytes, place = at % kRowBytes / 16;
+            const int r = r0 < left ? r0 : left;
+            ko[i] = (uint32_t)(r * (int)p.k_stride + k_piece<D>(r0, place) * 8) * 2u;
+            vo[i] = (uint32_t)(r * (int)p.v_stride + v_piece<D>(r0, place) * 8) * 2u;
+        }
+    };
+    places(kKeys, k_off, v_off);
+    const uint32_t lds_k = (uint32_t)(uintptr_t)&s_k[0][0] + wave * kLoads * 1024, lds_v = (uint32_t)(uintptr_t)&s_v[0][0] + wave * kLoads * 1024;
+    // Step tk of K and then step tv of V into their stages.  Past the end the last step again, so that every step
+    // counts the same loads; rows past the end repeat the last one: their weights are 0, their values finite.
+    const auto issue = [&](int tk, int tv, bool v) INLINE {
+        const uint32_t ks = lds_k + (tk & (kStages - 1)) * kTileBytes, vs = lds_v + (tv & (kStages - 1)) * kTileBytes;
+        tk = tk < steps ? tk : steps - 1;
+        tv = tv < steps ? tv : steps - 1;
+        const uint16_t *kb = kg + (int64_t)tk * kKeys * p.k_stride, *vb = vg + (int64_t)tv * kKeys * p.v_stride;
+        if (tk * kKeys + kKeys <= n) {  // tv <= tk
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) dma16(kb, k_off[i], ks + 1024 * i);
+            if (v) {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) dma16(vb, v_off[i], vs + 1024 * i);
+            }
+        } else {
+            uint32_t ko[kLoads], vo[kLoads], unused[kLoads];
+            places(n - 1 - tk * kKeys, ko, unused);
+            places(n - 1 - tv * kKeys, unused, vo);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) dma16(kb, ko[i], ks + 1024 * i);
+            if (v) {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) dma16(vb, vo[i], vs + 1024 * i);
+            }
+        }
+    };
+
+    issue(0, 0, false);
+    issue(1, 0, false);
+    v8bf qf[kK];
     {
         const int r = row < n ? row : n - 1;
         const uint16_t *qg = p.q + (n0 + r) * p.q_stride + (int64_t)head * D + 8 * half;
 #pragma unroll
-        for (int s = 0; s < kKSteps; ++s) qf[s] = *reinterpret_cast<const v8bf *>(qg + 16 * s);
-    }
-    const int seen = p.causal && q0 + kRows < n ? q0 + kRows : n;  // keys that any row of the workgroup sees
-    const int tiles = (seen + kKeys - 1) / kKeys;
-
-    v16f o[kDTiles];
+        for (int s = 0; s < kK; ++s) qf[s] = *reinterpret_cast<const v8bf *>(qg + 16 * s);
+        // Here: the compiler does not count the direct loads, and a wait for these in the loop, where it would put it, would be one for
+        // all of those at every step.
 #pragma unroll
-    for (int i = 0; i < kDTiles; ++i)
+        for (int s = 0; s < kK; ++s) asm volatile("" : "+v"(qf[s]));
+    }
+    issue(2, 0, true);
+    issue(3, 1, true);
+
+    v16f o[kD];
+    float m = 0.0f, l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kD; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
-    float m = -INFINITY, l = 0.0f;
 
-    v4u ks[kPieces], vs[kPieces];
-    const auto fetch = [&](int t) {
+    // operand reads from stage `stage`
+    int k_at[kK];
+    uint32_t v_at[kD];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int id = tid + i * 64 * kWaves, r = t * kKeys + id / (D / 8), ch = id % (D / 8);
-            if (r < n) {
-                ks[i] = *reinterpret_cast<const v4u *>(kg + r * p.k_stride + ch * 8);
-                vs[i] = *reinterpret_cast<const v4u *>(vg + r * p.v_stride + ch * 8);
-            } else {  // keys past the end: their weights are 0, so their values must be finite
-                ks[i] = v4u{0, 0, 0, 0};
-                vs[i] = v4u{0, 0, 0, 0};
+    for (int s = 0; s < kK; ++s) k_at[s] = col * kRowBytes + (k_piece<D>(col, 2 * s + half) << 4);
+    const int v_row = 4 * half + ((lane & 15) >> 2);
+#pragma unroll
+    for (int i = 0; i < kD; ++i) {
+        v_at[i] = (uint32_t)(uintptr_t)&s_v[0][0] + v_row * kRowBytes +
+                  (v_piece<D>(v_row, 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) << 4) + 8 * (lane & 1);
+        asm volatile("" : "+v"(v_at[i]));  // with the array's place in it, the rest fits the reads' 16-bit offset
+    }
+    const auto read_k = [&](int stage, int s) INLINE {  // channels 16 s .. +15
+        return *reinterpret_cast<const v8bf *>(&s_k[0][0] + k_at[s] + stage * kTileBytes);
+    };
+    const auto read_v = [&](int stage, int s, int i) INLINE {  // keys 16 s .. +15, channels 32 i .. +31, transposed
+        v4s f[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)  // 8 rows further on the places are the same
+            f[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_v4s *)(uintptr_t)(v_at[i] + (stage * kTileBytes + (16 * s + 8 * x) * kRowBytes)));
+        return __builtin_bit_cast(v8bf, __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    const auto hide = [&](v16f &s, int step) INLINE {  // keys that a row does not see
+        const int last = (p.causal && row < n - 1 ? row : n - 1) - kKeys * step - 4 * half;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (8 * (r / 4) + r % 4 > last) s[r] = -INFINITY;
+    };
+
+    constexpr int kAhead = 3;  // operand reads ahead of their product
+    v8bf kf[4], vf[4];
+    v16f s0, s1;
+    uint32_t p0[8], p1[8];
+
+    // One step: the weights of step j from its scores `sc` into `pc`, beside the scores of step j + 1 into `sn` and the
+    // second product of step j - 1 with its weights `pp`.  Written in the order in which it is to be issued: VALU work of a
+    // wave runs in the shadow of that wave's matrix products.  u = j % 4, a constant.
+    const auto body = [&](int j, int u, v16f &sc, v16f &sn, uint32_t (&pc)[8], uint32_t (&pp)[8]) INLINE {
+        float e[2] = {0.0f, 0.0f};
+        const auto pack = [&](int id) INLINE {  // weights id - 1 and id, a while after they were computed
+            pc[id / 2] = bf16_pair(e[0], e[1]);
+            l += e[0];
+            l += e[1];
+            asm volatile("" : "+v"(pc[id / 2]), "+v"(l));  // here, not behind the next branch
+        };
+        const auto weights = [&](int slot) INLINE {
+#pragma unroll
+            for (int c = 0; c < kScores; ++c) {
+                const int id = slot * kScores + c;
+                const float a = __builtin_fmaf(sc[id], p.scale2, -m);
+                if (id > 0 && id % 2 == 0) pack(id - 1);
+                e[id % 2] = __builtin_amdgcn_exp2f(a);
             }
+        };
+#pragma unroll
+        for (int s = 0; s < kK; ++s) {
+            if (s == 0) {
+                const v16f z = {0.0f};
+                sn = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[0], qf[0], z, 0, 0, 0);
+            } else {
+                sn = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s & 3], qf[s], sn, 0, 0, 0);
+            }
+            if (s + kAhead < kK)
+                kf[(s + kAhead) & 3] = read_k((u + 1) & 3, s + kAhead);
+            else
+                vf[s + kAhead - kK] = read_v((u + 3) & 3, (s + kAhead - kK) / kD, (s + kAhead - kK) % kD);
+            weights(s);
+            __builtin_amdgcn_sched_barrier(0);
         }
-    };
-    const auto stage = [&](int buf) {
+        float mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int id = tid + i * 64 * kWaves, r = id / (D / 8), ch = id % (D / 8);
-            *reinterpret_cast<v4u *>(s_k[buf] + k_at<D>(r, ch)) = ks[i];
-            *reinterpret_cast<v4u *>(s_v[buf] + v_at<D>(r, ch)) = vs[i];
-        }
-    };
-
-    fetch(0);
-    stage(0);
-    __syncthreads();
-    const int wave_seen = w0 >= n ? 0 : p.causal && w0 + kRowsWave < n ? w0 + kRowsWave : n;
-    for (int t = 0; t < tiles; ++t) {
-        const int buf = t & 1;
-        if (t + 1 < tiles) fetch(t + 1);
-        const int u0 = t * kKeys;
-        if (u0 < wave_seen) {
-            v16f s[2];
+        for (int s = 0; s < 2 * kD; ++s) {
+            const v4u w = {pp[4 * (s / kD)], pp[4 * (s / kD) + 1], pp[4 * (s / kD) + 2], pp[4 * (s / kD) + 3]};
+            o[s % kD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[s & 3], __builtin_bit_cast(v8bf, w), o[s % kD], 0, 0, 0);
+            const int a = s + kAhead;
+            if (a < 2 * kD)
+                vf[a & 3] = read_v((u + 3) & 3, a / kD, a % kD);
+            else
+                kf[a - 2 * kD] = read_k((u + 2) & 3, a - 2 * kD);
+            weights(kK + s);
+            if (s >= 2) {
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[tt][r] = 0.0f;
-#pragma unroll
-                for (int st = 0; st < kKSteps; ++st) {
-                    const v8bf a = *reinterpret_cast<const v8bf *>(s_k[buf] + k_at<D>(32 * tt + col, 2 * st + half));
-                    s[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[st], s[tt], 0, 0, 0);
+                for (int id = (s - 2) * 8 / (2 * kD - 2); id < (s - 1) * 8 / (2 * kD - 2); ++id) {
+                    mx = fmaxf(fmaxf(mx, sn[2 * id]), sn[2 * id + 1]);
+                    asm volatile("" : "+v"(mx));
                 }
             }
-            // a key is seen if it is in the sequence and, when causal, not behind the row
-            const int last = p.causal && row < n - 1 ? row : n - 1;
-            if (u0 + kKeys - 1 > (p.causal && w0 < n - 1 ? w0 : n - 1)) {
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        pack(15);
+        if (j + 1 >= whole) {  // the last steps of a row: not beside anything
+            hide(sn, j + 1);
+            mx = sn[0];
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (u0 + 32 * tt + 8 * (r / 4) + 4 * half + r % 4 > last) s[tt][r] = -INFINITY;
-            }
-            float mt = s[0][0];
-#pragma unroll
-            for (int r = 1; r < 32; ++r) mt = fmaxf(mt, s[r / 16][r % 16]);
-            mt = max_halves(mt) * p.scale2;
-            const float mn = fmaxf(m, mt);  // finite: a row sees key 0 in its first tile
+            for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sn[r]);
+        }
+        // the reference of the next step's weights
+        const float t = max_halves(mx) * p.scale2;
+        if (__any(t > m + kSlack)) {
+            const float mn = t > m + kSlack ? __builtin_ceilf(t) : m;
             const float alpha = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
-            uint32_t pw[16];
-            float sum = 0.0f;
+            l *= alpha;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r / 8][2 * r % 16], p.scale2, -mn));
-                const float c = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r / 8][2 * r % 16 + 1], p.scale2, -mn));
-                sum += a + c;
-                pw[r] = bf16_pair(a, c);
-            }
-            l = __builtin_fmaf(l, alpha, sum);
-#pragma unroll
-            for (int i = 0; i < kDTiles; ++i)
+            for (int i = 0; i < kD; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[i][r] *= alpha;
-            const int j = lane & 15;
 #pragma unroll
-            for (int st = 0; st < 4; ++st) {
-                const v4u w = {pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]};
-                const v8bf pf = __builtin_bit_cast(v8bf, w);
-#pragma unroll
-                for (int i = 0; i < kDTiles; ++i) {
-                    v4s f[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int r = 16 * st + 8 * x + 4 * half + (j >> 2);
-                        const int ch = 4 * i + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
-                        f[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(s_v[buf] + v_at<D>(r, ch) + 8 * (j & 1)));
-                    }
-                    const v8bf vf = __builtin_bit_cast(v8bf, __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[i], 0, 0, 0);
-                }
-            }
+            for (int i = 0; i < 8; ++i)  // weights of this step, not yet multiplied: a power of two leaves their digits
+                pc[i] = bf16_pair(__uint_as_float(pc[i] << 16) * alpha, __uint_as_float(pc[i] & 0xFFFF0000u) * alpha);
         }
-        if (t + 1 < tiles) stage(buf ^ 1);
-        __syncthreads();
+    };
+
+    // ---- step 0's scores
+    wait_loads_barrier<4 * kLoads>();
+    if (wave_steps > 0) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s0[r] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kK; ++s) s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(0, s), qf[s], s0, 0, 0, 0);
+        if (whole == 0) hide(s0, 0);
+        float t = s0[0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) t = fmaxf(t, s0[r]);
+        m = __builtin_ceilf(max_halves(t) * p.scale2);  // finite: every row sees key 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p1[i] = 0;  // no step before the first
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) kf[i] = read_k(1, i);
     }
+    // The first step multiplies weights 0 by stage 3 of V, which nothing has been loaded to yet: zeros, as 0 * x need not be 0.
+    for (int i = tid; i < kTileBytes / 16; i += 64 * kWaves) reinterpret_cast<v4u *>(s_v[3])[i] = v4u{0, 0, 0, 0};
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+
+    const auto step = [&](int j, int u) INLINE {  // u = j % 4, a constant
+        wait_loads_barrier<3 * kLoads>();
+        if (j < steps) issue(j + 4, j + 2, true);
+        if (j < wave_steps) {
+            if (u & 1)
+                body(j, u, s1, s0, p1, p0);
+            else
+                body(j, u, s0, s1, p0, p1);
+        } else if (j == wave_steps && j > 0) {  // the last step's second product
+            uint32_t (&pp)[8] = u & 1 ? p0 : p1;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < kD; ++i) {
+                    const v4u w = {pp[4 * s], pp[4 * s + 1], pp[4 * s + 2], pp[4 * s + 3]};
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v((u + 3) & 3, s, i), __builtin_bit_cast(v8bf, w), o[i], 0, 0, 0);
+                }
+        }
+    };
+    for (int j = 0; j <= steps; j += 4) {
+        step(j, 0);
+        if (j + 1 <= steps) step(j + 1, 1);
+        if (j + 2 <= steps) step(j + 2, 2);
+        if (j + 3 <= steps) step(j + 3, 3);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the end still write to LDS
 
     l = add_halves(l);
     if (row >= n) return;
     const float inv = 1.0f / l;
     uint16_t *og = p.out + ((n0 + row) * p.q_heads + head) * D + 4 * half;
 #pragma unroll
-    for (int i = 0; i < kDTiles; ++i)
+    for (int i = 0; i < kD; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint2 *>(og + 32 * i + 8 * j) =
@@ -215,7 +365,7 @@ extern "C" bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, c
     if (!heads_ok(q_heads, kv_heads) || !head_dim_ok(head_dim) || batch < 1 || batch > 65535 || tokens < 1 ||
         tokens > kMaxTokens || max_len < 1 || q_stride < (int64_t)q_heads * head_dim ||
         k_stride < (int64_t)kv_heads * head_dim || v_stride < (int64_t)kv_heads * head_dim || q_stride % 8 || k_stride % 8 ||
-        v_stride % 8)
+        v_stride % 8 || q_stride > kMaxStride || k_stride > kMaxStride || v_stride > kMaxStride)
         return BITNET_ERR_UNSUPPORTED_SHAPE;
     PromptArgs p;
     p.q = static_cast<const uint16_t *>(q); p.k = static_cast<const uint16_t *>(k); p.v = static_cast<const uint16_t *>(v);
@@ -225,7 +375,7 @@ extern "C" bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, c
     p.q_heads = q_heads; p.kv_heads = kv_heads; p.causal = causal ? 1 : 0;
     p.scale2 = scale * 1.44269504088896340736f;
     p.out = static_cast<uint16_t *>(out);
-    const dim3 grid((unsigned)((p.max_len + kRows - 1) / kRows), (unsigned)q_heads, (unsigned)batch);
+    const dim3 grid((unsigned)q_heads, (unsigned)batch, (unsigned)((p.max_len + kRows - 1) / kRows));
     if (head_dim == 64)
         hipLaunchKernelGGL((attn_prompt_kernel<64>), grid, dim3(64 * kWaves), 0, stream, p);
     else
