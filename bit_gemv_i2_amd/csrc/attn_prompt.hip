@@ -26,15 +26,15 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
-#ifndef OCC64
-#define OCC64 2
-#endif
 constexpr int kWaves = 4;
 constexpr int kRowsWave = 32;                 // query rows of a wave
-constexpr int kRows = kWaves * kRowsWave;     // and of a workgroup
 constexpr int kKeys = 32;                     // keys of a step
 constexpr int kStages = 4;                    // steps of K and of V in LDS
 constexpr float kSlack = 8.0f;                // log2 of the largest weight before a row's reference moves
+#ifndef FEW
+#define FEW 256
+#endif
+constexpr int64_t kFewGroups = FEW;
 constexpr int64_t kMaxTokens = 1 << 22;  // rows of workgroups of the launch inside 16 bits
 constexpr int64_t kMaxStride = 1 << 23;
 
@@ -82,17 +82,20 @@ __device__ __forceinline__ void wait_loads_barrier() {
 
 #define INLINE __attribute__((always_inline))
 
-template <int D>
-__global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_kernel(PromptArgs p) {
+// PARTS: the waves of a workgroup share its keys in 1 or 2 parts, every PARTS-th step each.
+template <int D, int PARTS>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs p) {
+    constexpr int kRowWaves = kWaves / PARTS;       // waves side by side in the rows
+    constexpr int kRows = kRowWaves * kRowsWave;    // query rows of a workgroup
     constexpr int kRowBytes = 2 * D;
     constexpr int kTileBytes = kKeys * kRowBytes;
     constexpr int kK = D / 16;              // products of a step's scores
     constexpr int kD = D / 32;              // channel tiles of the second product, two products each
     constexpr int kSlots = kK + 2 * kD;
     constexpr int kScores = 16 / kSlots;    // weights computed beside a product
-    constexpr int kLoads = kTileBytes / 1024 / kWaves;  // direct loads of a wave for a step of K (or V)
-    __shared__ __align__(1024) uint8_t s_k[kStages][kTileBytes];
-    __shared__ __align__(1024) uint8_t s_v[kStages][kTileBytes];
+    constexpr int kLoads = kTileBytes / 1024 / kRowWaves;  // direct loads of a wave for a step of K (or V)
+    __shared__ __align__(1024) uint8_t s_k[PARTS][kStages][kTileBytes];
+    __shared__ __align__(1024) uint8_t s_v[PARTS][kStages][kTileBytes];
 
     const int b = blockIdx.y, head = blockIdx.x;
     const int64_t n0 = p.starts[b], n1 = p.starts[b + 1];
@@ -106,20 +109,24 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_
     const uint16_t *kg = p.k + n0 * p.k_stride + (int64_t)hk * D;
     const uint16_t *vg = p.v + n0 * p.v_stride + (int64_t)hk * D;
 
-    const int w0 = q0 + wave * kRowsWave;  // this wave's first row
+    const int part = wave / kRowWaves, side = wave % kRowWaves;
+    const int w0 = q0 + side * kRowsWave;  // this wave's first row
     const int row = w0 + col;              // this lane's
     const int seen = p.causal && q0 + kRows < n ? q0 + kRows : n;  // keys that any row of the workgroup sees
-    const int steps = (seen + kKeys - 1) / kKeys;
+    const int last_step = (seen - 1) / kKeys;
     const int wave_seen = w0 >= n ? 0 : p.causal && w0 + kRowsWave < n ? w0 + kRowsWave : n;
-    const int wave_steps = (wave_seen + kKeys - 1) / kKeys;
-    const int whole = (p.causal && w0 + 1 < n ? w0 + 1 : n) / kKeys;  // steps that every row of the wave sees whole
+    // Steps from here on are a part's own: its step j is step PARTS j + part of the keys.
+    const auto own = [&](int all) INLINE { return (all - part + PARTS - 1) / PARTS; };  // its share of the first `all` steps
+    const int steps = last_step / PARTS + 1;
+    const int wave_steps = own((wave_seen + kKeys - 1) / kKeys);
+    const int whole = own((p.causal && w0 + 1 < n ? w0 + 1 : n) / kKeys);  // steps that every row of the wave sees whole
 
     // ---- direct loads: a lane's places in LDS are fixed, and with them its rows and pieces
     uint32_t k_off[kLoads], v_off[kLoads];
     const auto places = [&](int left, uint32_t (&ko)[kLoads], uint32_t (&vo)[kLoads]) INLINE {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int at = (wave * kLoads + i) * 1024 + lane * 16;
+            const int at = (side * kLoads + i) * 1024 + lane * 16;
             const int r0 = at / kRowBytes, place = at % kRowBytes / 16;
             const int r = r0 < left ? r0 : left;
             ko[i] = (uint32_t)(r * (int)p.k_stride + k_piece<D>(r0, place) * 8) * 2u;
@@ -127,13 +134,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_
         }
     };
     places(kKeys, k_off, v_off);
-    const uint32_t lds_k = (uint32_t)(uintptr_t)&s_k[0][0] + wave * kLoads * 1024, lds_v = (uint32_t)(uintptr_t)&s_v[0][0] + wave * kLoads * 1024;
+    const uint32_t lds_k = (uint32_t)(uintptr_t)&s_k[part][0][0] + side * kLoads * 1024;
+    const uint32_t lds_v = (uint32_t)(uintptr_t)&s_v[part][0][0] + side * kLoads * 1024;
     // Step tk of K and then step tv of V into their stages.  Past the end the last step again, so that every step
     // counts the same loads; rows past the end repeat the last one: their weights are 0, their values finite.
     const auto issue = [&](int tk, int tv, bool v) INLINE {
         const uint32_t ks = lds_k + (tk & (kStages - 1)) * kTileBytes, vs = lds_v + (tv & (kStages - 1)) * kTileBytes;
-        tk = tk < steps ? tk : steps - 1;
-        tv = tv < steps ? tv : steps - 1;
+        tk = PARTS * tk + part < last_step ? PARTS * tk + part : last_step;
+        tv = PARTS * tv + part < last_step ? PARTS * tv + part : last_step;
         const uint16_t *kb = kg + (int64_t)tk * kKeys * p.k_stride, *vb = vg + (int64_t)tv * kKeys * p.v_stride;
         if (tk * kKeys + kKeys <= n) {  // tv <= tk
 #pragma unroll
@@ -172,7 +180,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_
     issue(3, 1, true);
 
     v16f o[kD];
-    float m = 0.0f, l = 0.0f;
+    float m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int i = 0; i < kD; ++i)
 #pragma unroll
@@ -182,16 +190,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_
     int k_at[kK];
     uint32_t v_at[kD];
 #pragma unroll
-    for (int s = 0; s < kK; ++s) k_at[s] = col * kRowBytes + (k_piece<D>(col, 2 * s + half) << 4);
+    for (int s = 0; s < kK; ++s) k_at[s] = part * kStages * kTileBytes + col * kRowBytes + (k_piece<D>(col, 2 * s + half) << 4);
     const int v_row = 4 * half + ((lane & 15) >> 2);
 #pragma unroll
     for (int i = 0; i < kD; ++i) {
-        v_at[i] = (uint32_t)(uintptr_t)&s_v[0][0] + v_row * kRowBytes +
+        v_at[i] = (uint32_t)(uintptr_t)&s_v[part][0][0] + v_row * kRowBytes +
                   (v_piece<D>(v_row, 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) << 4) + 8 * (lane & 1);
         asm volatile("" : "+v"(v_at[i]));  // with the array's place in it, the rest fits the reads' 16-bit offset
     }
     const auto read_k = [&](int stage, int s) INLINE {  // channels 16 s .. +15
-        return *reinterpret_cast<const v8bf *>(&s_k[0][0] + k_at[s] + stage * kTileBytes);
+        return *reinterpret_cast<const v8bf *>(&s_k[0][0][0] + k_at[s] + stage * kTileBytes);
     };
     const auto read_v = [&](int stage, int s, int i) INLINE {  // keys 16 s .. +15, channels 32 i .. +31, transposed
         v4s f[2];
@@ -202,7 +210,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_
         return __builtin_bit_cast(v8bf, __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
     const auto hide = [&](v16f &s, int step) INLINE {  // keys that a row does not see
-        const int last = (p.causal && row < n - 1 ? row : n - 1) - kKeys * step - 4 * half;
+        const int last = (p.causal && row < n - 1 ? row : n - 1) - kKeys * (PARTS * step + part) - 4 * half;
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             if (8 * (r / 4) + r % 4 > last) s[r] = -INFINITY;
@@ -310,7 +318,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_
         for (int i = 0; i < kAhead; ++i) kf[i] = read_k(1, i);
     }
     // The first step multiplies weights 0 by stage 3 of V, which nothing has been loaded to yet: zeros, as 0 * x need not be 0.
-    for (int i = tid; i < kTileBytes / 16; i += 64 * kWaves) reinterpret_cast<v4u *>(s_v[3])[i] = v4u{0, 0, 0, 0};
+    for (int i = side * 64 + lane; i < kTileBytes / 16; i += 64 * kRowWaves) reinterpret_cast<v4u *>(s_v[part][3])[i] = v4u{0, 0, 0, 0};
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 
     const auto step = [&](int j, int u) INLINE {  // u = j % 4, a constant
@@ -341,6 +349,29 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the end still write to LDS
 
     l = add_halves(l);
+    if constexpr (PARTS == 2) {  // join the parts; the stages are free once every wave's loads are done
+        static_assert(kRowWaves * D * 32 * 4 <= sizeof(s_k), "a part's sums fit the stages");
+        __shared__ float s_ml[kRowWaves][64][2];
+        __syncthreads();
+        float *sums = reinterpret_cast<float *>(&s_k[0][0][0]) + side * (D / 2 * 64) + lane;
+        if (part == 1) {
+#pragma unroll
+            for (int i = 0; i < kD; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sums[(16 * i + r) * 64] = o[i][r];
+            s_ml[side][lane][0] = m;
+            s_ml[side][lane][1] = l;
+        }
+        __syncthreads();
+        if (part == 1) return;
+        const float m1 = s_ml[side][lane][0], mm = fmaxf(m, m1);  // a row sees key 0, in part 0: finite where row < n
+        const float a0 = __builtin_amdgcn_exp2f(m - mm), a1 = __builtin_amdgcn_exp2f(m1 - mm);
+        l = l * a0 + s_ml[side][lane][1] * a1;
+#pragma unroll
+        for (int i = 0; i < kD; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[i][r] = o[i][r] * a0 + sums[(16 * i + r) * 64] * a1;
+    }
     if (row >= n) return;
     const float inv = 1.0f / l;
     uint16_t *og = p.out + ((n0 + row) * p.q_heads + head) * D + 4 * half;
@@ -351,6 +382,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? OCC64 : 2) void attn_prompt_
             *reinterpret_cast<uint2 *>(og + 32 * i + 8 * j) =
                 make_uint2(bf16_pair(o[i][4 * j] * inv, o[i][4 * j + 1] * inv),
                            bf16_pair(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
+}
+
+template <int D, int PARTS>
+void launch_parts(const PromptArgs &p, int batch, hipStream_t stream) {
+    constexpr int rows = kWaves / PARTS * kRowsWave;
+    hipLaunchKernelGGL((attn_prompt_kernel<D, PARTS>), dim3(p.q_heads, batch, (p.max_len + rows - 1) / rows), dim3(64 * kWaves),
+                       0, stream, p);
+}
+
+template <int D>
+void launch_prompt(const PromptArgs &p, int batch, hipStream_t stream) {
+    const int64_t groups = (int64_t)p.q_heads * batch * ((p.max_len + kWaves * kRowsWave - 1) / (kWaves * kRowsWave));
+    if (groups <= kFewGroups)
+        launch_parts<D, 2>(p, batch, stream);
+    else
+        launch_parts<D, 1>(p, batch, stream);
 }
 
 }  // namespace
@@ -375,10 +422,9 @@ extern "C" bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, c
     p.q_heads = q_heads; p.kv_heads = kv_heads; p.causal = causal ? 1 : 0;
     p.scale2 = scale * 1.44269504088896340736f;
     p.out = static_cast<uint16_t *>(out);
-    const dim3 grid((unsigned)q_heads, (unsigned)batch, (unsigned)((p.max_len + kRows - 1) / kRows));
     if (head_dim == 64)
-        hipLaunchKernelGGL((attn_prompt_kernel<64>), grid, dim3(64 * kWaves), 0, stream, p);
+        launch_prompt<64>(p, batch, stream);
     else
-        hipLaunchKernelGGL((attn_prompt_kernel<128>), grid, dim3(64 * kWaves), 0, stream, p);
+        launch_prompt<128>(p, batch, stream);
     return launched();
 }
