@@ -22,19 +22,27 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) v8bf lds_v8bf;
+typedef __attribute__((address_space(3))) v4u lds_v4u;
+typedef __attribute__((address_space(3))) float lds_float;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 constexpr int kWaves = 4;
 constexpr int kRowsWave = 32;                 // query rows of a wave
 constexpr int kKeys = 32;                     // keys of a step
 constexpr int kStages = 4;                    // steps of K and of V in LDS
 constexpr float kSlack = 8.0f;                // log2 of the largest weight before a row's reference moves
-#ifndef FEW
-#define FEW 256
-#endif
-constexpr int64_t kFewGroups = FEW;
+// A launch of at most so many workgroups shares the keys of each between two halves of its waves, which doubles the workgroups: up
+// to where these no longer run at once.  20 heads of 128, one prompt: 512 tokens 12.8 us instead of 16.5, 1536 (240 workgroups)
+// 32.3 instead of 35.9, but 2048 (320) 52.6 instead of 48.9; 32 heads of 64: 512 tokens 9.3 instead of 12.9, 1536 (384) 24.8
+// instead of 29.6, 2048 (512) 38.5 instead of 39.1, 3000 (768) 68.1 instead of 64.2.  Two steps are too few to share
+// (64 tokens: 7.7 us instead of 6.6, 5.4 instead of 5.2).
+template <int D>
+constexpr int kFewGroups = D == 64 ? 512 : 256;
+constexpr int kShareFrom = 65;
 constexpr int64_t kMaxTokens = 1 << 22;  // rows of workgroups of the launch inside 16 bits
 constexpr int64_t kMaxStride = 1 << 23;
 
@@ -80,6 +88,7 @@ __device__ __forceinline__ void wait_loads_barrier() {
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// The loop's parts are lambdas called with constants for each of its four stages: left to itself the compiler makes them functions.
 #define INLINE __attribute__((always_inline))
 
 // PARTS: the waves of a workgroup share its keys in 1 or 2 parts, every PARTS-th step each.
@@ -94,8 +103,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
     constexpr int kSlots = kK + 2 * kD;
     constexpr int kScores = 16 / kSlots;    // weights computed beside a product
     constexpr int kLoads = kTileBytes / 1024 / kRowWaves;  // direct loads of a wave for a step of K (or V)
-    __shared__ __align__(1024) uint8_t s_k[PARTS][kStages][kTileBytes];
-    __shared__ __align__(1024) uint8_t s_v[PARTS][kStages][kTileBytes];
+    // Stages of K [PARTS][kStages][kTileBytes] and then of V.  Sized at the launch: at the 128 KiB of two parts of 128 channels the
+    // compiler would plan for one wave a SIMD and put the scores into accumulator registers, from which every one has to be moved.
+    extern __shared__ __align__(1024) uint8_t stages[];
+    constexpr int kPartBytes = kStages * kTileBytes;
+    const uint32_t lds = (uint32_t)(uintptr_t)(lds_u8 *)stages;
 
     const int b = blockIdx.y, head = blockIdx.x;
     const int64_t n0 = p.starts[b], n1 = p.starts[b + 1];
@@ -134,8 +146,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         }
     };
     places(kKeys, k_off, v_off);
-    const uint32_t lds_k = (uint32_t)(uintptr_t)&s_k[part][0][0] + side * kLoads * 1024;
-    const uint32_t lds_v = (uint32_t)(uintptr_t)&s_v[part][0][0] + side * kLoads * 1024;
+    const uint32_t part_k = lds + part * kPartBytes, part_v = part_k + PARTS * kPartBytes;  // this part's stages
+    const uint32_t lds_k = part_k + side * kLoads * 1024, lds_v = part_v + side * kLoads * 1024;
     // Step tk of K and then step tv of V into their stages.  Past the end the last step again, so that every step
     // counts the same loads; rows past the end repeat the last one: their weights are 0, their values finite.
     const auto issue = [&](int tk, int tv, bool v) INLINE {
@@ -187,19 +199,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
 
     // operand reads from stage `stage`
-    int k_at[kK];
-    uint32_t v_at[kD];
+    uint32_t k_at[kK], v_at[kD];
 #pragma unroll
-    for (int s = 0; s < kK; ++s) k_at[s] = part * kStages * kTileBytes + col * kRowBytes + (k_piece<D>(col, 2 * s + half) << 4);
+    for (int s = 0; s < kK; ++s) k_at[s] = part_k + col * kRowBytes + (k_piece<D>(col, 2 * s + half) << 4);
     const int v_row = 4 * half + ((lane & 15) >> 2);
 #pragma unroll
     for (int i = 0; i < kD; ++i) {
-        v_at[i] = (uint32_t)(uintptr_t)&s_v[part][0][0] + v_row * kRowBytes +
+        v_at[i] = part_v + v_row * kRowBytes +
                   (v_piece<D>(v_row, 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) << 4) + 8 * (lane & 1);
-        asm volatile("" : "+v"(v_at[i]));  // with the array's place in it, the rest fits the reads' 16-bit offset
     }
     const auto read_k = [&](int stage, int s) INLINE {  // channels 16 s .. +15
-        return *reinterpret_cast<const v8bf *>(&s_k[0][0][0] + k_at[s] + stage * kTileBytes);
+        return *(const lds_v8bf *)(uintptr_t)(k_at[s] + stage * kTileBytes);
     };
     const auto read_v = [&](int stage, int s, int i) INLINE {  // keys 16 s .. +15, channels 32 i .. +31, transposed
         v4s f[2];
@@ -318,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         for (int i = 0; i < kAhead; ++i) kf[i] = read_k(1, i);
     }
     // The first step multiplies weights 0 by stage 3 of V, which nothing has been loaded to yet: zeros, as 0 * x need not be 0.
-    for (int i = side * 64 + lane; i < kTileBytes / 16; i += 64 * kRowWaves) reinterpret_cast<v4u *>(s_v[part][3])[i] = v4u{0, 0, 0, 0};
+    for (int i = side * 64 + lane; i < kTileBytes / 16; i += 64 * kRowWaves) ((lds_v4u *)(uintptr_t)(part_v + 3 * kTileBytes))[i] = v4u{0, 0, 0, 0};
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 
     const auto step = [&](int j, int u) INLINE {  // u = j % 4, a constant
@@ -350,23 +360,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
 
     l = add_halves(l);
     if constexpr (PARTS == 2) {  // join the parts; the stages are free once every wave's loads are done
-        static_assert(kRowWaves * D * 32 * 4 <= sizeof(s_k), "a part's sums fit the stages");
-        __shared__ float s_ml[kRowWaves][64][2];
+        static_assert(kRowWaves * (D / 2 + 2) * 256 <= 2 * PARTS * kPartBytes, "a part's sums fit the stages");
         __syncthreads();
-        float *sums = reinterpret_cast<float *>(&s_k[0][0][0]) + side * (D / 2 * 64) + lane;
+        lds_float *sums = (lds_float *)(uintptr_t)lds + side * ((D / 2 + 2) * 64) + lane, *ml = sums + D / 2 * 64;
         if (part == 1) {
 #pragma unroll
             for (int i = 0; i < kD; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) sums[(16 * i + r) * 64] = o[i][r];
-            s_ml[side][lane][0] = m;
-            s_ml[side][lane][1] = l;
+            ml[0] = m;
+            ml[64] = l;
         }
         __syncthreads();
         if (part == 1) return;
-        const float m1 = s_ml[side][lane][0], mm = fmaxf(m, m1);  // a row sees key 0, in part 0: finite where row < n
+        const float m1 = ml[0], mm = fmaxf(m, m1);  // a row sees key 0, in part 0: finite where row < n
         const float a0 = __builtin_amdgcn_exp2f(m - mm), a1 = __builtin_amdgcn_exp2f(m1 - mm);
-        l = l * a0 + s_ml[side][lane][1] * a1;
+        l = l * a0 + ml[64] * a1;
 #pragma unroll
         for (int i = 0; i < kD; ++i)
 #pragma unroll
@@ -388,13 +397,13 @@ template <int D, int PARTS>
 void launch_parts(const PromptArgs &p, int batch, hipStream_t stream) {
     constexpr int rows = kWaves / PARTS * kRowsWave;
     hipLaunchKernelGGL((attn_prompt_kernel<D, PARTS>), dim3(p.q_heads, batch, (p.max_len + rows - 1) / rows), dim3(64 * kWaves),
-                       0, stream, p);
+                       2 * PARTS * kStages * kKeys * 2 * D, stream, p);
 }
 
 template <int D>
 void launch_prompt(const PromptArgs &p, int batch, hipStream_t stream) {
     const int64_t groups = (int64_t)p.q_heads * batch * ((p.max_len + kWaves * kRowsWave - 1) / (kWaves * kRowsWave));
-    if (groups <= kFewGroups)
+    if (groups <= kFewGroups<D> && p.max_len >= kShareFrom)
         launch_parts<D, 2>(p, batch, stream);
     else
         launch_parts<D, 1>(p, batch, stream);
