@@ -560,21 +560,31 @@ def bitnet_rope_table(positions: int, rot: int, base: float = 10000.0, factor: f
     return t
 
 
-def _cache_struct(k_cache, v_cache, k_scale, v_scale, table):
+_torch = None
+
+
+def _import_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _cache_struct(torch, k_cache, v_cache, k_scale, v_scale, table):
     """(bitnet_kv_cache_t over the given tensors, their device index), each tensor checked against the layout of the
     header.  One combined test first: a serving step makes this call for every layer."""
-    import torch
     i8, f32 = torch.int8, torch.float32
     dev = k_cache.get_device()
     if k_cache.dim() == 4 and table.dim() == 2:
         pages, heads, page, dim = k_cache.shape
-        batch, slots = table.shape
+        per_page = (pages, heads)
         if (k_cache.dtype is i8 and v_cache.dtype is i8 and k_scale.dtype is f32 and v_scale.dtype is f32
                 and table.dtype is torch.int32 and v_cache.shape == (pages, heads, dim, page)
-                and k_scale.shape == (pages, heads) and v_scale.shape == (pages, heads) and dev >= 0
+                and k_scale.shape == per_page and v_scale.shape == per_page
                 and dev == v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == table.get_device()
-                and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+                and dev >= 0 and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
                 and v_scale.is_contiguous() and table.is_contiguous()):
+            batch, slots = table.shape
             return KVCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                  table.data_ptr(), pages, heads, dim, page, batch, slots), dev
     # something is wrong: say what
@@ -604,10 +614,9 @@ def _on_device(t, name: str, dev: int, dtype=None, shape=None):
     return t.data_ptr()
 
 
-def _launch_stream(stream, dev: int):
+def _launch_stream(torch, stream, dev: int):
     """The stream handle of a launch on device `dev`, which has to be the current one."""
-    import torch
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         raise ValueError(f"the tensors are on device {dev}, the current device is {torch.cuda.current_device()}")
     # the handle alone: current_stream() builds an object around it, for as long as a launch takes
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
@@ -621,26 +630,27 @@ def _rows_ptr(t, name: str, inner: int, dev: int):
                          f"{name} must be on the device of the other tensors")
     if t.is_contiguous():
         return t.data_ptr(), inner
+    stride = t.stride()
+    if len(stride) == 3 and stride[2] == 1 and stride[1] == t.shape[2] and t.shape[0] > 1:
+        return t.data_ptr(), stride[0]
     want = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != want:
+    for size, step in zip(reversed(t.shape[1:]), reversed(stride[1:])):
+        if size != 1 and step != want:
             raise ValueError(f"{name} must have its heads and channels side by side in a row")
         want *= size
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else inner
+    return t.data_ptr(), stride[0] if t.shape[0] > 1 else inner
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory for a call on `stream`, taken from that stream's pool so that nothing still pending elsewhere
-    uses it."""
-    import torch
+def _empty(torch, like, shape, dtype, stream):
+    """Memory on `like`'s device for a call on `stream`, taken from that stream's pool so that nothing still pending
+    elsewhere uses it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _float_dt(t, name: str) -> int:
-    import torch
+def _float_dt(torch, t, name: str) -> int:
     if t.dtype is torch.bfloat16:
         return BITNET_DT_BF16
     if t.dtype is torch.float32:
@@ -655,9 +665,9 @@ def bitnet_rope_append_kv(qkv, rope, k_cache, v_cache, k_scale, v_scale, table, 
     positions and appends keys and values to the paged int8 cache.  rope: fp32 [positions][rot] on the device, or
     None; starts int32 [batch + 1], before int32 [batch].  Returns (q [T][q_heads][head_dim], k or None); k,
     the turned keys, is made when with_k or k_out asks for it."""
-    import torch
-    c, dev = _cache_struct(k_cache, v_cache, k_scale, v_scale, table)
-    dt = _float_dt(qkv, "qkv")
+    torch = _torch or _import_torch()
+    c, dev = _cache_struct(torch, k_cache, v_cache, k_scale, v_scale, table)
+    dt = _float_dt(torch, qkv, "qkv")
     hk, dim, batch = c.kv_heads, c.head_dim, c.batch
     width = (q_heads + 2 * hk) * dim
     if qkv.dim() != 2 or qkv.shape[1] != width:
@@ -674,17 +684,17 @@ def bitnet_rope_append_kv(qkv, rope, k_cache, v_cache, k_scale, v_scale, table, 
         rows, rot = rope.shape
     xp, stride = _rows_ptr(qkv, "qkv", width, dev)
     if q_out is None:
-        q_out = _empty((T, q_heads, dim), qkv.dtype, qkv.device, stream)
+        q_out = _empty(torch, qkv, (T, q_heads, dim), qkv.dtype, stream)
     else:
         _check(q_out, "q_out", qkv.dtype, numel=T * q_heads * dim)
     if k_out is not None:
         _check(k_out, "k_out", qkv.dtype, numel=T * hk * dim)
     elif with_k:
-        k_out = _empty((T, hk, dim), qkv.dtype, qkv.device, stream)
+        k_out = _empty(torch, qkv, (T, hk, dim), qkv.dtype, stream)
     _ok(lib().bitnet_rope_append_kv(xp, dt, stride, rp, rows, rot, bool(interleaved), sp, bp, T, max_new, q_heads,
                                     ctypes.byref(c), _on_device(q_out, "q_out", dev),
                                     None if k_out is None else _on_device(k_out, "k_out", dev),
-                                    _launch_stream(stream, dev)), "bitnet_rope_append_kv")
+                                    _launch_stream(torch, stream, dev)), "bitnet_rope_append_kv")
     return q_out, k_out
 
 
@@ -698,9 +708,9 @@ def bitnet_attn_decode(q, k_cache, v_cache, k_scale, v_scale, table, lengths, ma
     """Attention of one query token per sequence, q [batch][q_heads][head_dim], over the paged int8 cache; `lengths`
     int32 [batch] counts the cached tokens, max_len bounds them.  scale defaults to 1/sqrt(head_dim).  Returns
     [batch][q_heads][head_dim] in out_dtype (q's by default).  The workspace is allocated unless given."""
-    import torch
-    c, dev = _cache_struct(k_cache, v_cache, k_scale, v_scale, table)
-    qdt = _float_dt(q, "q")
+    torch = _torch or _import_torch()
+    c, dev = _cache_struct(torch, k_cache, v_cache, k_scale, v_scale, table)
+    qdt = _float_dt(torch, q, "q")
     batch, dim = c.batch, c.head_dim
     if q.dim() != 3 or q.shape[0] != batch or q.shape[2] != dim:
         raise ValueError(f"q must be [{batch}][q_heads][{dim}], not {tuple(q.shape)}")
@@ -708,13 +718,13 @@ def bitnet_attn_decode(q, k_cache, v_cache, k_scale, v_scale, table, lengths, ma
     qp, stride = _rows_ptr(q, "q", hq * dim, dev)
     lp = _on_device(lengths, "lengths", dev, torch.int32, (batch,))
     if out is None:
-        out = _empty((batch, hq, dim), out_dtype or q.dtype, q.device, stream)
+        out = _empty(torch, q, (batch, hq, dim), out_dtype or q.dtype, stream)
     else:
         _check(out, "out", out_dtype or out.dtype, numel=batch * hq * dim)
-    odt = _float_dt(out, "out")
+    odt = _float_dt(torch, out, "out")
     need = lib().bitnet_attn_decode_workspace_bytes(batch, hq, c.kv_heads, dim, max_len)
     if workspace is None and need:
-        workspace = _empty((need,), torch.uint8, q.device, stream)
+        workspace = _empty(torch, q, (need,), torch.uint8, stream)
     wp, nb = None, 0
     if workspace is not None:
         wp, nb = _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel()
@@ -722,7 +732,7 @@ def bitnet_attn_decode(q, k_cache, v_cache, k_scale, v_scale, table, lengths, ma
             raise ValueError(f"workspace must hold at least {need} bytes")
     _ok(lib().bitnet_attn_decode(qp, qdt, stride, ctypes.byref(c), lp, max_len, hq,
                                  dim ** -0.5 if scale is None else scale, _on_device(out, "out", dev), odt, wp, nb,
-                                 _launch_stream(stream, dev)), "bitnet_attn_decode")
+                                 _launch_stream(torch, stream, dev)), "bitnet_attn_decode")
     return out
 
 
@@ -731,7 +741,7 @@ def bitnet_attn_prompt(q, k, v, starts, max_len: int, causal: bool = True, scale
     """Attention over whole prompts packed one behind the other: q [T][q_heads][head_dim], k and v
     [T][kv_heads][head_dim], bf16, tokens at any stride; starts int32 [batch + 1], max_len the longest prompt.
     Returns bf16 [T][q_heads][head_dim]."""
-    import torch
+    torch = _torch or _import_torch()
     if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or v.shape != k.shape:
         raise ValueError("q must be [T][q_heads][head_dim], k and v [T][kv_heads][head_dim]")
     bf16 = torch.bfloat16
@@ -747,12 +757,12 @@ def bitnet_attn_prompt(q, k, v, starts, max_len: int, causal: bool = True, scale
     vp, vs = _rows_ptr(v, "v", hk * dim, dev)
     sp = _on_device(starts, "starts", dev, torch.int32)
     if out is None:
-        out = _empty((T, hq, dim), bf16, q.device, stream)
+        out = _empty(torch, q, (T, hq, dim), bf16, stream)
     else:
         _check(out, "out", bf16, numel=T * hq * dim)
     _ok(lib().bitnet_attn_prompt(qp, qs, kp, ks, vp, vs, sp, starts.shape[0] - 1, T, max_len, hq, hk, dim, bool(causal),
                                  dim ** -0.5 if scale is None else scale, _on_device(out, "out", dev),
-                                 _launch_stream(stream, dev)), "bitnet_attn_prompt")
+                                 _launch_stream(torch, stream, dev)), "bitnet_attn_prompt")
     return out
 
 
