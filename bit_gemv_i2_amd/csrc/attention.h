@@ -28,7 +28,7 @@ inline bitnet_status_t check_cache(const bitnet_kv_cache_t *c) {
     if (!c || !at(c->k, 16) || !at(c->v, 16) || !at(c->k_scale, 4) || !at(c->v_scale, 4) || !at(c->table, 4))
         return BITNET_ERR_INVALID_ARG;
     if (!head_dim_ok(c->head_dim) || !page_ok(c->page) || c->pages < 1 || c->pages > INT32_MAX || c->kv_heads < 1 ||
-        c->batch < 1 || c->batch > 65535 || c->slots < 1 || (int64_t)c->slots * c->page > INT32_MAX)
+        c->batch < 1 || c->batch > 65535 || c->slots < 1 || (int64_t)c->slots * c->page > (1 << 30))
         return BITNET_ERR_UNSUPPORTED_SHAPE;
     return BITNET_OK;
 }

@@ -1,7 +1,7 @@
 // Attention over whole prompts, packed one behind the other, bf16 on the matrix cores.
 //
 // out_t = sum_u p_u v_u / sum_u p_u, p_u = exp(scale * q_t.k_u - m): one pass over the keys with the
-// running maximum m and sum of the row, so that no score leaves the registers.
+// running reference m and sum of the row, so that no score leaves the registers.
 //
 // Both products are taken transposed: S^T = K Q^T and O^T = V^T P^T, with
 // v_mfma_f32_32x32x16_bf16.  A lane then holds one query row (lane % 32) and 16 of its scores for
@@ -9,6 +9,18 @@
 // half-waves and no other, and a lane's scores, rounded to bf16, are its own operand of the second
 // product, if that product takes its 16 keys in the order 8x + 4 (lane / 32) + r.  V^T is read from LDS by
 // the transposing 16-bit read, which gives a lane 4 keys of one channel: that same order.
+//
+// A wave has 32 rows and runs one software pipeline over steps of 32 keys: beside the 16 products (128 channels) that make
+// the scores of step j + 1 and add step j - 1 to the sums, it turns the scores of step j into weights, one a
+// product.  K and V come by direct loads into a ring of four steps, two to three steps ahead.
+//
+// What bounds it (8192 tokens, 20 / 5 heads of 128, causal: 344 us, 1.00 PFLOP/s, 77% of what the library's largest
+// bf16 product reaches here; 9 prompts of up to 2047 tokens, 32 / 8 heads of 64: 104 us, 0.62 PFLOP/s).  The matrix cores are busy
+// for 57% of the cycles at 128 channels, at a clock that falls from 2.4 to about 1.9 GHz under the load.  A step of one wave
+// alone takes some 1400 cycles, 512 of them products: the issue of its 250 instructions, the direct loads (a quarter), the
+// step's end with its reference and barrier.  Two waves a SIMD hide half of that.  Measured and not kept: 64 rows a wave
+// (half the LDS reads, but one wave a SIMD: 420 us), 8 waves sharing a ring (369), operands read 5 products ahead
+// (352), the reference checked beside the next step's first products (364), steps of 64 keys at 64 channels (109).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -43,8 +55,8 @@ constexpr float kSlack = 8.0f;                // log2 of the largest weight befo
 template <int D>
 constexpr int kFewGroups = D == 64 ? 512 : 256;
 constexpr int kShareFrom = 65;
-constexpr int64_t kMaxTokens = 1 << 22;  // rows of workgroups of the launch inside 16 bits
-constexpr int64_t kMaxStride = 1 << 23;
+constexpr int64_t kMaxTokens = 1 << 22;  // the launch's third dimension stays inside 16 bits
+constexpr int64_t kMaxStride = 1 << 23;  // a lane's offset inside a step stays inside 32 bits
 
 struct PromptArgs {
     const uint16_t *q, *k, *v;
@@ -82,7 +94,9 @@ __device__ __forceinline__ void dma16(const void *base, uint32_t offset, uint32_
         : "memory");
 }
 
-// Waits until at most N of this wave's direct loads are pending, then meets the workgroup.
+// Waits until at most N of this wave's direct loads are pending, then meets the workgroup.  At the top of step j, K up to step
+// j + 2 and V up to step j - 1 have to be there; after them only V of step j and the two of step j - 1's issue may be pending.  The
+// issue that follows takes the stages of K j and V j - 2, whose reads were consumed by products of step j - 1.
 template <int N>
 __device__ __forceinline__ void wait_loads_barrier() {
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -133,7 +147,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
     const int wave_steps = own((wave_seen + kKeys - 1) / kKeys);
     const int whole = own((p.causal && w0 + 1 < n ? w0 + 1 : n) / kKeys);  // steps that every row of the wave sees whole
 
-    // ---- direct loads: a lane's places in LDS are fixed, and with them its rows and pieces
+    // ---- direct loads (no staging registers and no LDS stores): a lane's places in LDS are fixed, and with them its rows and pieces
     uint32_t k_off[kLoads], v_off[kLoads];
     const auto places = [&](int left, uint32_t (&ko)[kLoads], uint32_t (&vo)[kLoads]) INLINE {
 #pragma unroll
@@ -293,7 +307,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
 #pragma unroll
             for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sn[r]);
         }
-        // the reference of the next step's weights
+        // The reference m follows the largest score only when that leaves it by more than kSlack: weights up to 2^kSlack lose
+        // nothing in bf16 or fp32, and the sums are scaled again a few times a row instead of at every step.  It is a whole
+        // number, so that a change is a power of two, exact also in weights already rounded.
         const float t = max_halves(mx) * p.scale2;
         if (__any(t > m + kSlack)) {
             const float mn = t > m + kSlack ? __builtin_ceilf(t) : m;
@@ -348,6 +364,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
                     const v4u w = {pp[4 * s], pp[4 * s + 1], pp[4 * s + 2], pp[4 * s + 3]};
                     o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v((u + 3) & 3, s, i), __builtin_bit_cast(v8bf, w), o[i], 0, 0, 0);
                 }
+            __builtin_amdgcn_sched_barrier(0);  // the reads are done with before the next barrier gives their stage away
         }
     };
     for (int j = 0; j <= steps; j += 4) {

@@ -437,7 +437,7 @@ bitnet_status_t bitnet_w2a8_gemv_lut(const uint8_t *packed, const float *scales,
  *              end are not read.  An entry outside 0 .. pages - 1 is never followed:
  *              nothing is stored there, and attention sees no token of that page.
  * A page belongs to one sequence while it is appended to; sequences may share pages that
- * are only read.  Scales are finite and >= 0. */
+ * are only read.  Scales are finite and >= 0.  slots * page <= 2^30. */
 typedef struct {
     int8_t *k, *v;
     float *k_scale, *v_scale;
@@ -527,8 +527,8 @@ bitnet_status_t bitnet_attn_decode(const void *q, int qdt, int64_t q_stride, con
  *   starts   device, int32 [batch + 1]
  *   max_len  the longest sequence; of a longer one only the first max_len rows take part
  *   out      device, bf16 [tokens][q_heads][head_dim]; rows of no sequence are not written
- * out must not overlap q, k or v.  Rules: strides >= the row and multiples of 8; scale > 0 and finite;
- * head_dim 64 or 128; kv_heads divides q_heads <= 1024; batch <= 65535; 1 <= tokens <= 2^24. */
+ * out must not overlap q, k or v.  Rules: strides >= the row, multiples of 8 and <= 2^23; scale > 0 and finite;
+ * head_dim 64 or 128; kv_heads divides q_heads <= 1024; batch <= 65535; 1 <= tokens <= 2^22. */
 bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                                    int64_t v_stride, const int32_t *starts, int batch, int64_t tokens, int max_len,
                                    int q_heads, int kv_heads, int head_dim, int causal, float scale, void *out,

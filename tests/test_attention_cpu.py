@@ -87,7 +87,7 @@ def _cache(**kw):
 BAD_CACHES = [(dict(k=NULL), ARG), (dict(v=MIS), ARG), (dict(k_scale=NULL), ARG), (dict(v_scale=MIS4), ARG), (dict(table=NULL), ARG),
               (dict(pages=0), SHAPE), (dict(pages=1 << 31), SHAPE), (dict(kv_heads=0), SHAPE), (dict(head_dim=96), SHAPE),
               (dict(page=24), SHAPE), (dict(page=256), SHAPE), (dict(batch=0), SHAPE), (dict(batch=65536), SHAPE),
-              (dict(slots=0), SHAPE), (dict(slots=1 << 28), SHAPE)]
+              (dict(slots=0), SHAPE), (dict(slots=1 << 28), SHAPE), (dict(slots=(1 << 26) + 1), SHAPE)]
 
 
 def _append(cache=None, **kw):
@@ -156,7 +156,8 @@ def test_prompt_refusals():
     for kw in (dict(q=NULL), dict(k=MIS), dict(v=NULL), dict(out=NULL), dict(starts=MIS4), dict(scale=0.0), dict(scale=math.nan)):
         assert _prompt(**kw) == ARG, kw
     for kw in (dict(qs=248), dict(qs=260), dict(ks=120), dict(vs=132), dict(batch=0), dict(batch=65536), dict(tokens=0),
-               dict(tokens=(1 << 24) + 1), dict(max_len=0), dict(q_heads=3), dict(kv_heads=0), dict(head_dim=32), dict(head_dim=256)):
+               dict(tokens=(1 << 22) + 1), dict(qs=(1 << 23) + 8), dict(vs=(1 << 23) + 8), dict(max_len=0), dict(q_heads=3), dict(kv_heads=0),
+               dict(head_dim=32), dict(head_dim=256)):
         assert _prompt(**kw) == SHAPE, kw
 
 
