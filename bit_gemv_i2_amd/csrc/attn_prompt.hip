@@ -308,11 +308,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
             for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sn[r]);
         }
         // The reference m follows the largest score only when that leaves it by more than kSlack: weights up to 2^kSlack lose
-        // nothing in bf16 or fp32, and the sums are scaled again a few times a row instead of at every step.  It is a whole
-        // number, so that a change is a power of two, exact also in weights already rounded.
+        // nothing in bf16 or fp32, and the sums are scaled again a few times a row instead of at every step.  It moves by a
+        // whole number, so that the scaling is by a power of two and leaves the digits of weights already rounded.
         const float t = max_halves(mx) * p.scale2;
         if (__any(t > m + kSlack)) {
-            const float mn = t > m + kSlack ? __builtin_ceilf(t) : m;
+            const float mn = t > m + kSlack ? m + __builtin_ceilf(t - m) : m;
             const float alpha = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= alpha;
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[i][r] *= alpha;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)  // weights of this step, not yet multiplied: a power of two leaves their digits
+            for (int i = 0; i < 8; ++i)  // weights of this step, not yet multiplied
                 pc[i] = bf16_pair(__uint_as_float(pc[i] << 16) * alpha, __uint_as_float(pc[i] & 0xFFFF0000u) * alpha);
         }
     };
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         float t = s0[0];
 #pragma unroll
         for (int r = 1; r < 16; ++r) t = fmaxf(t, s0[r]);
-        m = __builtin_ceilf(max_halves(t) * p.scale2);  // finite: every row sees key 0
+        m = max_halves(t) * p.scale2;  // finite: every row sees key 0
 #pragma unroll
         for (int i = 0; i < 8; ++i) p1[i] = 0;  // no step before the first
 #pragma unroll
