@@ -73,7 +73,7 @@ struct PromptArgs {
 // takes one piece of each of 16 rows at a time; for V, 64 bytes of each of 4 rows.
 template <int D>
 __device__ __forceinline__ int k_piece(int row, int ch) {
-    return ch ^ (row & (D / 8 - 1));
+    return ch ^ (D == 128 ? row & 15 : (row >> 1) & 7);  // (at 64 channels two rows share the 256 bytes of the banks)
 }
 template <int D>
 __device__ __forceinline__ int v_piece(int row, int ch) {
