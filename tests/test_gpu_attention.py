@@ -225,6 +225,15 @@ def test_decode_head_groups(gpu, hq, hk):
     _decode_case(np.random.default_rng(hq), hq, hk, 128, 16, "float32", "float32", [100, 33], wide=40)
 
 
+@pytest.mark.parametrize("hq,hk", [(5, 1), (16, 2), (12, 1), (36, 2)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_decode_groups_of_more_than_four(gpu, hq, hk, dim, page):
+    rng = np.random.default_rng(hq + page)
+    _decode_case(rng, hq, hk, dim, page, "float32", "float32", [1, 0, 17, 64, 300])
+    _decode_case(rng, hq, hk, dim, page, "bfloat16", "bfloat16", [2500, 63])
+
+
 @pytest.mark.parametrize("page", [16, 128])
 @pytest.mark.parametrize("odt", ["bfloat16", "float32"])
 def test_decode_long_contexts_are_split_and_joined(gpu, page, odt):
@@ -263,15 +272,16 @@ def test_decode_pages_that_do_not_exist_are_not_seen(gpu):
         _decode_case(rng, 4, 2, 64, 16, "float32", "float32", [90, 96], cache=c, table=table)
 
 
-def test_decode_non_finite_scales_and_stale_codes_behind_the_end(gpu):
+@pytest.mark.parametrize("hq", [4, 12])
+def test_decode_non_finite_scales_and_stale_codes_behind_the_end(gpu, hq):
     """Only what a sequence's length covers counts: pages of nobody have NaN and infinite scales, and the codes behind the
     last token of a page are those of an earlier owner."""
     rng = np.random.default_rng(14)
     c = ao.Cache(9, 2, 128, 32, rng)
     c.ks[[0, 8]], c.vs[[0, 8]] = np.nan, np.inf
     table = np.array([[3, 5, 8, 0], [1, 2, 0, 8]])
-    _decode_case(rng, 4, 2, 128, 32, "float32", "float32", [33, 64], cache=c, table=table)
-    _decode_case(rng, 4, 2, 128, 32, "bfloat16", "bfloat16", [64, 1], cache=c, table=table)
+    _decode_case(rng, hq, 2, 128, 32, "float32", "float32", [33, 64], cache=c, table=table)
+    _decode_case(rng, hq, 2, 128, 32, "bfloat16", "bfloat16", [64, 1], cache=c, table=table)
 
 
 def test_decode_pages_of_zeros(gpu):
@@ -288,7 +298,8 @@ def test_decode_pages_of_zeros(gpu):
     _decode_case(rng, 2, 1, 64, 16, "bfloat16", "float32", [100], cache=c, table=table, q=np.zeros((1, 2, 64)))
 
 
-def test_decode_one_large_weight_beside_a_long_flat_tail(gpu):
+@pytest.mark.parametrize("hq", [1, 6])
+def test_decode_one_large_weight_beside_a_long_flat_tail(gpu, hq):
     """A first token whose weight is thousands of times any other's, which together weigh as much: the tail must not be
     rounded away."""
     rng = np.random.default_rng(16)
@@ -302,11 +313,11 @@ def test_decode_one_large_weight_beside_a_long_flat_tail(gpu):
     c.k[:, :, :, 1:] = c.k[:, :, :, 1:] // 16
     c.k[0, 0, 0, 1:] = 0
     c.v = np.abs(c.v)  # so that a lost tail shows
-    q = np.zeros((1, 1, dim))
-    q[0, 0, 0] = 8.7 / (127 * 0.02 * dim ** -0.5)
-    q[0, 0, 1:] = rng.standard_normal(dim - 1) * 0.2
+    q = np.zeros((1, hq, dim))
+    q[0, :, 0] = 8.7 / (127 * 0.02 * dim ** -0.5)
+    q[0, :, 1:] = rng.standard_normal((hq, dim - 1)) * 0.2
     for odt in ("bfloat16", "float32"):
-        _decode_case(rng, 1, 1, dim, page, "float32", odt, [n], cache=c, table=table, q=q)
+        _decode_case(rng, hq, 1, dim, page, "float32", odt, [n], cache=c, table=table, q=q)
 
 
 def test_decode_scores_far_apart(gpu):
