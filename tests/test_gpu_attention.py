@@ -240,6 +240,13 @@ def test_decode_long_contexts_are_split_and_joined(gpu, page, odt):
     _decode_case(np.random.default_rng(9), 3, 1, 64, page, "float32", odt, [9000, 1, 0, 257, 4096])
 
 
+@pytest.mark.parametrize("hq,dim,page", [(4, 64, 16), (12, 64, 64), (4, 128, 32), (12, 128, 16)])
+def test_decode_of_large_caches_reads_past_the_memory_side_cache(gpu, hq, dim, page):
+    """The bound on the lengths says more than 256 MB, which takes the streaming loads, whatever the lengths are."""
+    rng = np.random.default_rng(hq + dim)
+    _decode_case(rng, hq, 2, dim, page, "float32", "float32", [9000, 700, 0, 15], max_len=600_000)
+
+
 def test_decode_single_long_row(gpu):
     _decode_case(np.random.default_rng(10), 4, 1, 128, 64, "bfloat16", "bfloat16", [20001])
 
@@ -412,6 +419,20 @@ def test_prompt_lengths(gpu, dim, causal, n):
 @pytest.mark.parametrize("dim", [64, 128])
 def test_prompt_packed_with_strides(gpu, hq, hk, causal, dim):
     _prompt_case(np.random.default_rng(hq), hq, hk, dim, [130, 1, 0, 64, 300, 17], causal, wide=24)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_many_workgroups(gpu, dim, causal):
+    """Enough workgroups that none shares its keys between its waves."""
+    rng = np.random.default_rng(20 + dim)
+    lens = [500, 1, 31, 32, 33, 64, 65, 127, 128, 129, 160, 255, 256, 257, 400, 0] + [int(x) for x in rng.integers(1, 500, 24)]
+    _prompt_case(rng, 4, 2, dim, lens, causal, wide=8)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_long_with_many_heads(gpu, dim):
+    _prompt_case(np.random.default_rng(30 + dim), 40, 8, dim, [1700], True)
 
 
 def test_prompt_many_short_sequences(gpu):
