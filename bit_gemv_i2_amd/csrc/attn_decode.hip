@@ -436,9 +436,15 @@ __global__ __launch_bounds__(kJoinRuns *D / 4) void attn_join_kernel(DecodeArgs 
 // wide and 367 narrow, of 16 184 and 741).
 int heads_of(int group) { return group <= 4 ? 4 : 16; }
 
+// Contexts of so few tiles are not cut: a tile more for each wave costs 1.25 us, the join 2.8 and, where the host launches it, a
+// call's other 4.  One sequence, 20 / 5 heads of 128: 768 tokens whole 7.9 us (8.0 cut) in a graph, 10.4 (14.6) called;
+// 1024 tokens 9.0 (8.1) and 10.3 (14.6); 1536 tokens 11.6 (8.2) and 11.7 (14.3).
+constexpr int kWhole = 4 * kWaves;
+
 // Tiles of one workgroup.  The longest contexts are cut so that all workgroups are resident at once
 // (one more than that would double the time), but no finer than a tile for each wave.
 int chunk_of(int batch, int kv_heads, int group, int tiles) {
+    if (tiles <= kWhole) return kWhole;
     const int heads = heads_of(group);
     const int64_t rows = (int64_t)batch * kv_heads * ((group + heads - 1) / heads);
     const int64_t splits = rows < kWantGroups ? kWantGroups / rows : 1;
