@@ -37,7 +37,7 @@ using namespace bitnet_attn;
 namespace {
 
 // What bounds it: the cache's bytes.  64 x 8192 tokens, 32 / 8 heads of 128: 1.08 GB in 171 us, 6.3 TB/s, 98% of a bare read;
-// one sequence of 131071 tokens, 20 / 5 heads: 168 MB in 34 us (4.9 TB/s) and 4 us to join 98 splits; 16 sequences
+// one sequence of 131071 tokens, 20 / 5 heads: 168 MB in 35 us (4.8 TB/s) and 4 us to join 98 splits; 16 sequences
 // of up to 4000: 42 MB in 14 us and 4 to join, the chain of a wave's three tiles: 2 us to the first keys
 // (lengths, pages, keys), then 2 to 3 a tile.  A tile takes some 340 VALU operations of a wave, 1400 cycles; a SIMD's share of
 // the bandwidth brings one in 5800.

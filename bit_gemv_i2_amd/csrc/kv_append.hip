@@ -5,9 +5,10 @@
 // inside one workgroup: the new values stay in registers between the maximum and the
 // codes, so the projection is read once.
 //
-// What bounds it: the bytes for long prompts (14733 tokens in 8 sequences, 32 / 8 heads of 128, bf16: 489 MB in 108 us,
-// 4.5 TB/s, 95% of a large copy's rate); for one token a chain of four loads, each behind the one before (the sequence's
-// bounds, its page, the projection and the scale, the reduction), 4.4 us of which an empty launch takes about half.
+// What bounds it: the bytes for long prompts (19713 tokens in 8 sequences, 32 / 8 heads of 128, bf16, the turned keys written
+// out as well: 489 MB in 107 us, 4.6 TB/s, 96% of a large copy's rate); for one token a chain of four loads, each behind the
+// one before (the sequence's bounds, its page, the projection and the scale, the reduction), 4.4 us of which an empty
+// launch takes about half.
 //
 // The arithmetic is specified operation by operation (include/bitnet_w2a8.h), so this
 // file must not contract products and sums into fused ones.
@@ -26,7 +27,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = 1 << 24;  // keeps the launch's thread count inside 32 bits
 // Query heads of one workgroup: they share the table row's loads, but a workgroup for each of few heads spreads over more
-// CUs.  512 tokens, 20 / 20 heads of 128: 1 head 7.8 us, 2 7.7, 4 9.4, 8 13.4; 14733 tokens, 32 / 8 heads: 116, 108, 111, 111.
+// CUs.  512 tokens, 20 / 20 heads of 128: 1 head 7.8 us, 2 7.7, 4 9.4, 8 13.4; 19713 tokens, 32 / 8 heads: 116, 108, 111, 111.
 constexpr int kQHeads = 2;
 
 struct AppendArgs {
