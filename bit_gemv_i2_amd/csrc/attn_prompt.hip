@@ -80,18 +80,37 @@ __device__ __forceinline__ int v_piece(int row, int ch) {
     return ch ^ (D == 128 ? (row & 3) << 2 : (row & 2) << 1);
 }
 
-// 16 bytes a lane from global memory (base + offset) to LDS at lds + 16 * lane.  M0 carries the LDS address.
-__device__ __forceinline__ void dma16(const void *base, uint32_t offset, uint32_t lds) {
+// N direct loads, 16 bytes a lane: load i from base + offset[i] + 1024 i to lds + 1024 i + 16 * lane (the load's own offset counts on
+// both sides).  M0 carries the LDS address; the compiler's is put back.
+template <int N>
+__device__ __forceinline__ void dma(const void *base, const uint32_t (&offset)[N], uint32_t lds) {
+    static_assert(N == 1 || N == 2 || N == 4);
     uint32_t saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %2, %3\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(lds), "v"(offset), "s"(base)
-        : "memory");
+    if constexpr (N == 1)
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %2, %3\n\t"
+                     "s_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "s"(lds), "v"(offset[0]), "s"(base)
+                     : "memory");
+    else if constexpr (N == 2)
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %2, %4\n\t"
+                     "global_load_lds_dwordx4 %3, %4 offset:1024\n\t"
+                     "s_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "s"(lds), "v"(offset[0]), "v"(offset[1]), "s"(base)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %2, %6\n\t"
+                     "global_load_lds_dwordx4 %3, %6 offset:1024\n\t"
+                     "global_load_lds_dwordx4 %4, %6 offset:2048\n\t"
+                     "global_load_lds_dwordx4 %5, %6 offset:3072\n\t"
+                     "s_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "s"(lds), "v"(offset[0]), "v"(offset[1]), "v"(offset[2]), "v"(offset[3]), "s"(base)
+                     : "memory");
 }
 
 // Waits until at most N of this wave's direct loads are pending, then meets the workgroup.  At the top of step j, K up to step
@@ -148,49 +167,49 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
     const int whole = own((p.causal && w0 + 1 < n ? w0 + 1 : n) / kKeys);  // steps that every row of the wave sees whole
 
     // ---- direct loads (no staging registers and no LDS stores): a lane's places in LDS are fixed, and with them its rows and pieces
-    uint32_t k_off[kLoads], v_off[kLoads];
-    const auto places = [&](int left, uint32_t (&ko)[kLoads], uint32_t (&vo)[kLoads]) INLINE {
+    const int r_first = (side * kLoads * 1024 + lane * 16) / kRowBytes, place = lane * 16 % kRowBytes / 16;
+    constexpr int kRowsLoad = 1024 / kRowBytes;  // rows of a load
+    uint32_t k_off[kLoads], v_off[kLoads];       // less the 1024 i that load i adds itself: it is that many bytes of rows on, or more
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int at = (side * kLoads + i) * 1024 + lane * 16;
-            const int r0 = at / kRowBytes, place = at % kRowBytes / 16;
-            const int r = r0 < left ? r0 : left;
-            ko[i] = (uint32_t)(r * (int)p.k_stride + k_piece<D>(r0, place) * 8) * 2u;
-            vo[i] = (uint32_t)(r * (int)p.v_stride + v_piece<D>(r0, place) * 8) * 2u;
-        }
-    };
-    places(kKeys, k_off, v_off);
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = r_first + kRowsLoad * i;
+        k_off[i] = (uint32_t)(r * (int)p.k_stride + k_piece<D>(r, place) * 8) * 2u - 1024 * i;
+        v_off[i] = (uint32_t)(r * (int)p.v_stride + v_piece<D>(r, place) * 8) * 2u - 1024 * i;
+    }
     const uint32_t part_k = lds + part * kPartBytes, part_v = part_k + PARTS * kPartBytes;  // this part's stages
     const uint32_t lds_k = part_k + side * kLoads * 1024, lds_v = part_v + side * kLoads * 1024;
-    // Step tk of K and then step tv of V into their stages.  Past the end the last step again, so that every step
-    // counts the same loads; rows past the end repeat the last one: their weights are 0, their values finite.
-    const auto issue = [&](int tk, int tv, bool v) INLINE {
-        const uint32_t ks = lds_k + (tk & (kStages - 1)) * kTileBytes, vs = lds_v + (tv & (kStages - 1)) * kTileBytes;
-        tk = PARTS * tk + part < last_step ? PARTS * tk + part : last_step;
-        tv = PARTS * tv + part < last_step ? PARTS * tv + part : last_step;
-        const uint16_t *kb = kg + (int64_t)tk * kKeys * p.k_stride, *vb = vg + (int64_t)tv * kKeys * p.v_stride;
-        if (tk * kKeys + kKeys <= n) {  // tv <= tk
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) dma16(kb, k_off[i], ks + 1024 * i);
-            if (v) {
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) dma16(vb, v_off[i], vs + 1024 * i);
-            }
+    // Step t of K (V) into its stage.  Past the end the last step again, so that every step counts the same loads; rows past
+    // the end repeat the last one: their weights are 0, their values finite.
+    const auto issue = [&](int t, const uint16_t *g, int64_t stride, const uint32_t (&offset)[kLoads], uint32_t to) INLINE {
+        to += (t & (kStages - 1)) * kTileBytes;
+        t = PARTS * t + part < last_step ? PARTS * t + part : last_step;
+        g += (int64_t)t * kKeys * stride;
+        const int left = n - 1 - t * kKeys;
+        if (left >= kKeys - 1) {
+            dma(g, offset, to);
         } else {
-            uint32_t ko[kLoads], vo[kLoads], unused[kLoads];
-            places(n - 1 - tk * kKeys, ko, unused);
-            places(n - 1 - tv * kKeys, unused, vo);
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) dma16(kb, ko[i], ks + 1024 * i);
-            if (v) {
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) dma16(vb, vo[i], vs + 1024 * i);
+            for (int i = 0; i < kLoads; ++i) {
+                const int back = r_first + kRowsLoad * i - left;
+                const uint32_t one[1] = {offset[i] + 1024 * i - (back > 0 ? (uint32_t)(back * (int)stride) * 2u : 0)};
+                dma(g, one, to + 1024 * i);
             }
         }
     };
+    const auto issue_k = [&](int t) INLINE { issue(t, kg, p.k_stride, k_off, lds_k); };
+    const auto issue_v = [&](int t) INLINE { issue(t, vg, p.v_stride, v_off, lds_v); };
+    // The loop's loads, step j + 4 of K and j + 2 of V, take the next place of running pointers as long as step j + 4 is a whole one.
+    const int quick = own(n / kKeys < last_step + 1 ? n / kKeys : last_step + 1) - 4;
+    const uint16_t *k_next = kg + (4 * PARTS + part) * kKeys * p.k_stride, *v_next = vg + (2 * PARTS + part) * kKeys * p.v_stride;
+    const auto issue_next = [&](int u) INLINE {  // u = j % 4
+        dma(k_next, k_off, lds_k + u * kTileBytes);
+        dma(v_next, v_off, lds_v + ((u + 2) & 3) * kTileBytes);
+        k_next += PARTS * kKeys * p.k_stride;
+        v_next += PARTS * kKeys * p.v_stride;
+    };
 
-    issue(0, 0, false);
-    issue(1, 0, false);
+    issue_k(0);
+    issue_k(1);
     v8bf qf[kK];
     {
         const int r = row < n ? row : n - 1;
@@ -202,8 +221,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
 #pragma unroll
         for (int s = 0; s < kK; ++s) asm volatile("" : "+v"(qf[s]));
     }
-    issue(2, 0, true);
-    issue(3, 1, true);
+    issue_k(2);
+    issue_v(0);
+    issue_k(3);
+    issue_v(1);
 
     v16f o[kD];
     float m = -INFINITY, l = 0.0f;
@@ -349,7 +370,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
 
     const auto step = [&](int j, int u) INLINE {  // u = j % 4, a constant
         wait_loads_barrier<3 * kLoads>();
-        if (j < steps) issue(j + 4, j + 2, true);
+        if (j < quick) {
+            issue_next(u);
+        } else if (j < steps) {
+            issue_k(j + 4);
+            issue_v(j + 2);
+        }
         if (j < wave_steps) {
             if (u & 1)
                 body(j, u, s1, s0, p1, p0);
