@@ -528,7 +528,8 @@ bitnet_status_t bitnet_attn_decode(const void *q, int qdt, int64_t q_stride, con
  *   max_len  the longest sequence; of a longer one only the first max_len rows take part
  *   out      device, bf16 [tokens][q_heads][head_dim]; rows of no sequence are not written
  * out must not overlap q, k or v.  Rules: strides >= the row, multiples of 8 and <= 2^23; scale > 0 and finite;
- * head_dim 64 or 128; kv_heads divides q_heads <= 1024; batch <= 65535; 1 <= tokens <= 2^22. */
+ * head_dim 64 or 128; kv_heads divides q_heads <= 1024; batch <= 65535; 1 <= tokens <= 2^22;
+ * batch * kv_heads * ceil(min(max_len, tokens) / 128) <= 2^30. */
 bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                                    int64_t v_stride, const int32_t *starts, int batch, int64_t tokens, int max_len,
                                    int q_heads, int kv_heads, int head_dim, int causal, float scale, void *out,

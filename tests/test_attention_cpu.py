@@ -157,7 +157,7 @@ def test_prompt_refusals():
         assert _prompt(**kw) == ARG, kw
     for kw in (dict(qs=248), dict(qs=260), dict(ks=120), dict(vs=132), dict(batch=0), dict(batch=65536), dict(tokens=0),
                dict(tokens=(1 << 22) + 1), dict(qs=(1 << 23) + 8), dict(vs=(1 << 23) + 8), dict(max_len=0), dict(q_heads=3), dict(kv_heads=0),
-               dict(head_dim=32), dict(head_dim=256)):
+               dict(head_dim=32), dict(head_dim=256), dict(batch=65535, tokens=1 << 22, max_len=1 << 22)):
         assert _prompt(**kw) == SHAPE, kw
 
 

@@ -460,6 +460,17 @@ def test_prompt_longer_than_the_grid_of_one_pass(gpu):
     _prompt_case(np.random.default_rng(26), 1, 1, 64, [1100, 3, 900], False, scale=0.05)
 
 
+@pytest.mark.parametrize("hq,hk,dim", [(20, 5, 128), (6, 3, 64), (8, 8, 64)])
+def test_prompt_tiles_over_the_dies(gpu, hq, hk, dim):
+    _prompt_case(np.random.default_rng(29), hq, hk, dim, [300, 7, 0, 150, 129], True)
+
+
+def test_prompt_more_tiles_than_one_dimension_of_a_launch_holds(gpu):
+    lens = [0] * 65535
+    lens[0], lens[40000], lens[65534] = 5, 70, 1100
+    _prompt_case(np.random.default_rng(30), 1, 1, 64, lens, True)
+
+
 def test_prompt_starts_that_make_no_sense_touch_nothing(gpu):
     """Ends before beginnings, past the tokens or below 0: such a sequence is left out."""
     rng = np.random.default_rng(27)
