@@ -650,6 +650,12 @@ def _empty(torch, like, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _bound(n: int, name: str):
+    """ctypes would cut a count to its low 32 bits without a word."""
+    if n > 0x7FFFFFFF:
+        raise ValueError(f"{name} must be below 2^31")
+
+
 def _float_dt(torch, t, name: str) -> int:
     if t.dtype is torch.bfloat16:
         return BITNET_DT_BF16
@@ -666,6 +672,7 @@ def bitnet_rope_append_kv(qkv, rope, k_cache, v_cache, k_scale, v_scale, table, 
     None; starts int32 [batch + 1], before int32 [batch].  Returns (q [T][q_heads][head_dim], k or None); k,
     the turned keys, is made when with_k or k_out asks for it."""
     torch = _torch or _import_torch()
+    _bound(max_new, "max_new")
     c, dev = _cache_struct(torch, k_cache, v_cache, k_scale, v_scale, table)
     dt = _float_dt(torch, qkv, "qkv")
     hk, dim, batch = c.kv_heads, c.head_dim, c.batch
@@ -699,6 +706,7 @@ def bitnet_rope_append_kv(qkv, rope, k_cache, v_cache, k_scale, v_scale, table, 
 
 
 def bitnet_attn_decode_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int) -> int:
+    _bound(max_len, "max_len")
     return lib().bitnet_attn_decode_workspace_bytes(int(batch), int(q_heads), int(kv_heads), int(head_dim),
                                                     int(max_len))
 
@@ -709,6 +717,7 @@ def bitnet_attn_decode(q, k_cache, v_cache, k_scale, v_scale, table, lengths, ma
     int32 [batch] counts the cached tokens, max_len bounds them.  scale defaults to 1/sqrt(head_dim).  Returns
     [batch][q_heads][head_dim] in out_dtype (q's by default).  The workspace is allocated unless given."""
     torch = _torch or _import_torch()
+    _bound(max_len, "max_len")
     c, dev = _cache_struct(torch, k_cache, v_cache, k_scale, v_scale, table)
     qdt = _float_dt(torch, q, "q")
     batch, dim = c.batch, c.head_dim
@@ -742,6 +751,7 @@ def bitnet_attn_prompt(q, k, v, starts, max_len: int, causal: bool = True, scale
     [T][kv_heads][head_dim], bf16, tokens at any stride; starts int32 [batch + 1], max_len the longest prompt.
     Returns bf16 [T][q_heads][head_dim]."""
     torch = _torch or _import_torch()
+    _bound(max_len, "max_len")
     if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or v.shape != k.shape:
         raise ValueError("q must be [T][q_heads][head_dim], k and v [T][kv_heads][head_dim]")
     bf16 = torch.bfloat16

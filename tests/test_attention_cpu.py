@@ -201,6 +201,22 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     assert c.k.numel() == c.v.numel() == bn.bitnet_kv_cache_bytes(4, 2, 64, 16)
 
 
+def test_binding_refuses_counts_past_32_bits():
+    """ctypes keeps the low 32 bits of an int without a word: 2^32 + 5 would become a bound of 5."""
+    import torch
+    h, i3 = _host(), torch.zeros(3, dtype=torch.int32)
+    b = torch.zeros(5, 4, 64, dtype=torch.bfloat16)
+    for n in (1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError, match="max_len"):
+            bn.bitnet_attn_decode(torch.zeros(3, 4, 64), *h.values(), i3, n)
+        with pytest.raises(ValueError, match="max_len"):
+            bn.bitnet_attn_decode_workspace_bytes(3, 4, 2, 64, n)
+        with pytest.raises(ValueError, match="max_len"):
+            bn.bitnet_attn_prompt(b, b, b, i3, n)
+        with pytest.raises(ValueError, match="max_new"):
+            bn.bitnet_rope_append_kv(torch.zeros(5, 8 * 64), None, *h.values(), i3, i3, n, 4)
+
+
 def test_rows_may_be_slices_of_wider_rows_but_not_strided_inside():
     import torch
 
