@@ -86,6 +86,14 @@ __device__ __forceinline__ float dpp_add(float v) {
 // The sum over a quad of lanes, the same bits in each.
 __device__ __forceinline__ float quad_sum(float v) { return dpp_add<0x4E>(dpp_add<0xB1>(v)); }
 
+// The largest of the four lanes that hold a query row.
+__device__ __forceinline__ uint32_t max_row(uint32_t v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    const uint32_t u = r[0] > r[1] ? r[0] : r[1];
+    const auto t = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return t[0] > t[1] ? t[0] : t[1];
+}
+
 constexpr uint32_t digit_sel(int i) { return 0x0C0C0000u | (uint32_t)(4 + i) << 8 | (uint32_t)i; }
 
 // Digit sums, digit 0 lowest, as one fp32 value.
@@ -184,7 +192,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
     const float weight = WIDE ? 1.0f : __uint_as_float((uint32_t)(127 + 8 * dg) << 23);  // 256^dg
     {
         float f[kSteps][16];
-        float most = 0.0f;
+        uint32_t top = 0;  // magnitude bits: an infinity or a NaN is larger than any number
         const bool there = head < heads;
         const int64_t at = b * p.q_stride + (int64_t)(head0 + (there ? head : 0)) * D + 16 * g;
         const auto load_row = [&](const auto *q) {
@@ -204,12 +212,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 f[s][e] = there ? f[s][e] : 0.0f;
-                most = fmaxf(most, fabsf(f[s][e]));
+                const uint32_t u = __float_as_uint(f[s][e]) & 0x7FFFFFFFu;
+                top = top > u ? top : u;
             }
-        most = max_halves(max_rows16(most));
+        top = max_row(top);
+        const float most = __uint_as_float(top);
         int ex;
         (void)frexpf(most, &ex);  // most < 2^ex, so |value| <= 2^30 and its top digit is within +-64
-        qunit = ldexpf(p.scale2 * weight, ex - 30);
+        // a row with an infinity or a NaN has no digits: its scores and its output become NaN
+        qunit = top < 0x7F800000u ? ldexpf(p.scale2 * weight, ex - 30) : __uint_as_float(0x7FC00000u);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -370,7 +381,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
         }
         const int64_t row = (int64_t)b * p.q_heads + head0 + col;
         if (p.splits == 1) {
-            store_out(p, row * D + d, ll > 0.0f ? oo / ll : 0.0f);
+            store_out(p, row * D + d, ll != 0.0f ? oo / ll : 0.0f);
         } else {
             p.part[(row * p.splits + split) * D + d] = oo;
             if (d == 0) {
@@ -426,7 +437,7 @@ __global__ __launch_bounds__(kJoinRuns *D / 4) void attn_join_kernel(DecodeArgs 
             sum += s_o[r][i];
             w += s_l[r];
         }
-        store_out(p, row * D + i, w > 0.0f ? sum / w : 0.0f);
+        store_out(p, row * D + i, w != 0.0f ? sum / w : 0.0f);
     }
 }
 

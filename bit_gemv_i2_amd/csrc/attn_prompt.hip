@@ -36,6 +36,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef unsigned short v2u16 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) v8bf lds_v8bf;
 typedef __attribute__((address_space(3))) v4u lds_v4u;
@@ -376,6 +377,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
     for (int i = side * 64 + lane; i < kTileBytes / 16; i += 64 * kRowWaves) ((lds_v4u *)(uintptr_t)(part_v + 3 * kTileBytes))[i] = v4u{0, 0, 0, 0};
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 
+    bool odd = false;  // the wave's last step has values that are infinite or NaN
     const auto step = [&](int j, int u) INLINE {  // u = j % 4, a constant
         wait_loads_barrier<3 * kLoads>();
         if (j < quick) {
@@ -391,13 +393,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
                 body(j, u, s0, s1, p0, p1);
         } else if (j == wave_steps && j > 0) {  // the last step's second product
             uint32_t (&pp)[8] = u & 1 ? p0 : p1;
+            v2u16 most = {0, 0};
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < kD; ++i) {
                     const v4u w = {pp[4 * s], pp[4 * s + 1], pp[4 * s + 2], pp[4 * s + 3]};
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v((u + 3) & 3, s, i), __builtin_bit_cast(v8bf, w), o[i], 0, 0, 0);
+                    const v8bf f = read_v((u + 3) & 3, s, i);
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, __builtin_bit_cast(v8bf, w), o[i], 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        most = __builtin_elementwise_max(most, __builtin_bit_cast(v2u16, __builtin_bit_cast(v4u, f)[e] & 0x7FFF7FFFu));
                 }
+            odd = __any(most[0] >= 0x7F80 || most[1] >= 0x7F80);
             __builtin_amdgcn_sched_barrier(0);  // the reads are done with before the next barrier gives their stage away
         }
     };
@@ -411,9 +419,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
 
     l = add_halves(l);
     if constexpr (PARTS == 2) {  // join the parts; the stages are free once every wave's loads are done
-        static_assert(kRowWaves * (D / 2 + 2) * 256 <= 2 * PARTS * kPartBytes, "a part's sums fit the stages");
+        static_assert(kRowWaves * (D / 2 + 3) * 256 <= 2 * PARTS * kPartBytes, "a part's sums fit the stages");
         __syncthreads();
-        lds_float *sums = (lds_float *)(uintptr_t)lds + side * ((D / 2 + 2) * 64) + lane, *ml = sums + D / 2 * 64;
+        lds_float *sums = (lds_float *)(uintptr_t)lds + side * ((D / 2 + 3) * 64) + lane, *ml = sums + D / 2 * 64;
         if (part == 1) {
 #pragma unroll
             for (int i = 0; i < kD; ++i)
@@ -421,9 +429,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
                 for (int r = 0; r < 16; ++r) sums[(16 * i + r) * 64] = o[i][r];
             ml[0] = m;
             ml[64] = l;
+            ml[128] = odd ? 1.0f : 0.0f;
         }
         __syncthreads();
         if (part == 1) return;
+        odd |= __any(ml[128] != 0.0f);
         const float m1 = ml[0], mm = fmaxf(m, m1);  // a row sees key 0, in part 0: finite where row < n
         const float a0 = __builtin_amdgcn_exp2f(m - mm), a1 = __builtin_amdgcn_exp2f(m1 - mm);
         l = l * a0 + ml[64] * a1;
@@ -431,6 +441,43 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         for (int i = 0; i < kD; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[i][r] = o[i][r] * a0 + sums[(16 * i + r) * 64] * a1;
+    }
+    // The last step has keys that some of its rows do not see.  Their weight is 0, which hides a finite value only: if there are others
+    // among them, these rows are taken again one by one.  (Seldom and slow: a lane a key, then a lane a channel.)
+    if (odd) {
+        for (int r = w0; r < w0 + kRowsWave && r < n; ++r) {
+            const uint16_t *qr = p.q + (n0 + r) * p.q_stride + (int64_t)head * D;
+            const int keys = p.causal ? r + 1 : n;
+            const auto score = [&](int key) {
+                float s = 0.0f;
+                for (int c = 0; c < D; c += 8) {
+                    float a[8], b[8];
+                    load8(qr + c, a);
+                    load8(kg + key * p.k_stride + c, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(a[e], b[e], s);
+                }
+                return s * p.scale2;
+            };
+            float top = -INFINITY, sum = 0.0f, out[D / 64] = {};
+            for (int key = lane; key < keys; key += 64) top = fmaxf(top, score(key));
+            for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+            for (int first = 0; first < keys; first += 64) {
+                const float e = first + lane < keys ? __builtin_amdgcn_exp2f(score(first + lane) - top) : 0.0f;
+                sum += e;
+                for (int x = 0; x < 64 && first + x < keys; ++x) {
+                    const float weight = __shfl(e, x);
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+                        out[i] = __builtin_fmaf(weight, __uint_as_float((uint32_t)vg[(first + x) * p.v_stride + 64 * i + lane] << 16), out[i]);
+                }
+            }
+            for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+                p.out[((n0 + r) * p.q_heads + head) * D + 64 * i + lane] = (uint16_t)bf16_pair(out[i] / sum, 0.0f);
+        }
+        return;
     }
     if (row >= n) return;
     const float inv = 1.0f / l;

@@ -476,6 +476,7 @@ bitnet_status_t bitnet_rope_table(int64_t positions, int rot, double base, doubl
  *   codes, if their scale grew, become rint(code * (old / new)); a new code is
  *   clamp(rint(x * (1 / scale)), -127, 127).  (fp32, half to even, correctly rounded divisions.)
  *   Codes of positions that no token has yet are left as they are.
+ *   A NaN is stored as code -127; an infinity makes its page's scale infinite, and what attention then reads there NaN.
  *   qkv      device, [tokens][(q_heads + 2 kv_heads) * head_dim], queries, keys, values;
  *            dt BITNET_DT_BF16 or BITNET_DT_F32; rows `row_stride` elements apart
  *   rope     device, fp32 [rope_rows][rot] (bitnet_rope_table)
@@ -502,7 +503,7 @@ bitnet_status_t bitnet_rope_append_kv(const void *qkv, int dt, int64_t row_strid
  * taken as sums of int8 digits to the base 256 (q: 30 bits below the row's largest value, weights: 23 bits below
  * the largest of their 64), summed exactly in int32; statistics and sums over blocks are fp32.
  *   q          device, [batch][q_heads][head_dim], qdt BITNET_DT_BF16 or BITNET_DT_F32, sequences
- *              `q_stride` elements apart
+ *              `q_stride` elements apart; a row with an infinity or a NaN gives a row of NaN
  *   lengths    device, int32 [batch]: tokens in the cache, the current one included; a length
  *              above max_len or slots * page is read as that, one below 1 gives zeros
  *   out        device, [batch][q_heads][head_dim], odt BITNET_DT_BF16 or BITNET_DT_F32
@@ -518,7 +519,7 @@ bitnet_status_t bitnet_attn_decode(const void *q, int qdt, int64_t q_stride, con
 /* Attention over whole prompts, packed one behind the other: sequence b is rows
  * starts[b] .. starts[b+1] - 1 of q, k, v and out;
  *     out[t][i] = sum_u softmax_u(scale * q[t][i] . k[u]) v[u]
- * over the u of the same sequence, u <= t when causal.  bf16 in and out; scores, softmax
+ * over the u of the same sequence, u <= t when causal (infinities and NaN at other u do not matter).  bf16 in and out; scores, softmax
  * statistics and sums are fp32, the weights are rounded to bf16 for the matrix cores (their
  * sum is taken before that rounding).
  *   q        device, bf16 [tokens][q_heads][head_dim], tokens q_stride elements apart

@@ -368,7 +368,57 @@ def test_decode_cache_past_32_bit_offsets(gpu):
         assert float(ks[pid, 0]) == float(ref.ks[i, 0]) and float(vs[pid, 0]) == float(ref.vs[i, 0])
 
 
+@pytest.mark.parametrize("hq,n,where", [(4, 100, 1), (4, 5000, 2), (16, 300, 5), (16, 5000, 0)])
+def test_decode_query_rows_that_are_not_finite_give_nan_and_only_they(gpu, hq, n, where):
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(31)
+    cache = ao.Cache((n + 63) // 64, 1, 128, 64, rng)
+    table = np.arange((n + 63) // 64)[None]
+    for bad in (np.nan, np.inf, -np.inf):
+        qd, q64 = _as(rng.standard_normal((1, hq, 128)), "float32")
+        qd[0, where, 77] = bad
+        out = bn.bitnet_attn_decode(qd, *(torch.from_numpy(a).cuda() for a in (cache.k, cache.v, cache.ks, cache.vs)), _int(table), _int([n]), n)
+        torch.cuda.synchronize()
+        got = out.double().cpu().numpy()
+        want, tol = ao.decode(q64, cache, table, [n], 128 ** -0.5, True, 30)
+        assert np.isnan(got[0, where]).all()
+        keep = np.arange(hq) != where
+        assert np.all(np.abs(got - want)[:, keep] <= tol[:, keep])
+
+
 # ------------------------------------------------------------------ prompt
+@pytest.mark.parametrize("hq,hk", [(2, 1), (40, 40)])  # keys shared between halves of the waves, and not
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_values_that_are_not_finite_behind_a_row(gpu, hq, hk, dim, causal):
+    """A weight of 0 must not meet an infinity: rows in front of it, also those of its own 32 keys, are as if it were not there."""
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(32)
+    lens = [300, 70, 1030 if hq == 40 else 97]
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    T = int(starts[-1])
+    (qd, q), (kd, k), (vd, v) = (_as(rng.standard_normal((T, h, dim)), "bfloat16") for h in (hq, hk, hk))
+    places = [(0, 170, 3, np.inf), (0, 187, 9, -np.inf), (0, 188, 9, np.inf), (1, 69, 5, np.nan), (1, 40, 60, -np.inf), (2, 95, 0, np.inf)]
+    want, tol, _ = ao.prompt(q, k, v, starts.tolist(), causal, dim ** -0.5, max(lens))
+    group = hq // hk
+    for b, u, ch, x in places:
+        vd[starts[b] + u, hk - 1, ch] = x
+        rows = slice(starts[b] + u if causal else starts[b], starts[b + 1])
+        want[rows, hq - group:, ch] += x
+    out = bn.bitnet_attn_prompt(qd, kd, vd, _int(starts), max(lens), causal=causal)
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    odd = ~np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[odd & ~np.isnan(want)], want[odd & ~np.isnan(want)])
+    fine, worst = ao.within(got[~odd], want[~odd], tol[~odd], True)
+    assert fine, worst
+
+
 def _prompt_case(rng, hq, hk, dim, lens, causal, wide=0, max_len=None, gain=1.0, poison=(), scale=None, starts=None):
     import torch
 
