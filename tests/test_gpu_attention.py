@@ -368,6 +368,23 @@ def test_decode_cache_past_32_bit_offsets(gpu):
         assert float(ks[pid, 0]) == float(ref.ks[i, 0]) and float(vs[pid, 0]) == float(ref.vs[i, 0])
 
 
+@pytest.mark.parametrize("group", [1, 8])
+@pytest.mark.parametrize("part", ["key", "value"])
+def test_an_infinity_that_was_appended_is_seen(gpu, part, group):
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(33)
+    hk, hq, dim, n = 2, 2 * group, 64, 200
+    c = bn.KVCache.empty(4, hk, dim, 64)
+    x = torch.from_numpy(rng.standard_normal((n, hq + 2 * hk, dim)).astype(np.float32)).cuda()
+    x[130, hq + 1 + (hk if part == "value" else 0), 7] = np.inf  # of key head 1
+    q, _ = c.append(x.flatten(1), None, _int([[0, 1, 2, 3]]), _int([0, n]), _int([0]), n, hq)
+    out = c.attend(q[:1], _int([[0, 1, 2, 3]]), _int([n]), n)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out[0, :group]).all()) and not bool(torch.isfinite(out[0, group:]).any())
+
+
 @pytest.mark.parametrize("hq,n,where", [(4, 100, 1), (4, 5000, 2), (16, 300, 5), (16, 5000, 0)])
 def test_decode_query_rows_that_are_not_finite_give_nan_and_only_they(gpu, hq, n, where):
     import torch
@@ -408,7 +425,8 @@ def test_prompt_values_that_are_not_finite_behind_a_row(gpu, hq, hk, dim, causal
     for b, u, ch, x in places:
         vd[starts[b] + u, hk - 1, ch] = x
         rows = slice(starts[b] + u if causal else starts[b], starts[b + 1])
-        want[rows, hq - group:, ch] += x
+        with np.errstate(invalid="ignore"):
+            want[rows, hq - group:, ch] += x
     out = bn.bitnet_attn_prompt(qd, kd, vd, _int(starts), max(lens), causal=causal)
     torch.cuda.synchronize()
     got = out.double().cpu().numpy()
