@@ -14,13 +14,14 @@
 // the scores of step j + 1 and add step j - 1 to the sums, it turns the scores of step j into weights, one a
 // product.  K and V come by direct loads into a ring of four steps, two to three steps ahead.
 //
-// What bounds it (8192 tokens, 20 / 5 heads of 128, causal: 344 us, 1.00 PFLOP/s, 77% of what the library's largest
-// bf16 product reaches here; 9 prompts of up to 2047 tokens, 32 / 8 heads of 64: 104 us, 0.62 PFLOP/s).  The matrix cores are busy
-// for 57% of the cycles at 128 channels, at a clock that falls from 2.4 to about 1.9 GHz under the load.  A step of one wave
-// alone takes some 1400 cycles, 512 of them products: the issue of its 250 instructions, the direct loads (a quarter), the
+// What bounds it (8192 tokens, 20 / 5 heads of 128, causal: 335 us, 1.03 PFLOP/s, 79% of what the library's largest
+// bf16 product reaches here; 9 prompts of up to 2047 tokens, 32 / 8 heads of 64: 98 us, 0.66 PFLOP/s).  The matrix cores are busy
+// for 60% of the cycles at 128 channels, at a clock that falls from 2.4 to about 1.9 GHz under the load.  A step of one wave
+// alone takes some 1400 cycles, 512 of them products: the issue of its 220 instructions, the direct loads (a quarter), the
 // step's end with its reference and barrier.  Two waves a SIMD hide half of that.  Measured and not kept: 64 rows a wave
-// (half the LDS reads, but one wave a SIMD: 420 us), 8 waves sharing a ring (369), operands read 5 products ahead
-// (352), the reference checked beside the next step's first products (364), steps of 64 keys at 64 channels (109).
+// (half the LDS reads, but one wave a SIMD: 420 us against 350 at the time), 8 waves sharing a ring (369), operands read 5
+// products ahead (352), the reference checked beside the next step's first products (364), steps of 64 keys at 64 channels (109
+// against 106); wave priorities and all first loads ahead of the queries (no change).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -49,10 +50,10 @@ constexpr int kKeys = 32;                     // keys of a step
 constexpr int kStages = 4;                    // steps of K and of V in LDS
 constexpr float kSlack = 8.0f;                // log2 of the largest weight before a row's reference moves
 // A launch of at most so many workgroups shares the keys of each between two halves of its waves, which doubles the workgroups: up
-// to where these no longer run at once.  20 heads of 128, one prompt: 512 tokens 12.8 us instead of 16.5, 1536 (240 workgroups)
-// 32.3 instead of 35.9, but 2048 (320) 52.6 instead of 48.9; 32 heads of 64: 512 tokens 9.3 instead of 12.9, 1536 (384) 24.8
-// instead of 29.6, 2048 (512) 38.5 instead of 39.1, 3000 (768) 68.1 instead of 64.2.  Two steps are too few to share
-// (64 tokens: 7.7 us instead of 6.6, 5.4 instead of 5.2).
+// to where these no longer run at once.  20 heads of 128, one prompt: 512 tokens 12.4 us instead of 16.1, 1536 (240 workgroups)
+// 31.1 instead of 34.2, but 2048 (320) 51.0 instead of 46.8; 32 heads of 64: 512 tokens 9.3 instead of 12.7, 1536 (384) 25.4
+// instead of 28.4, 2048 (512) 36.1 instead of 37.2, 3000 (768) 65 instead of 58.6.  Two steps are too few to share
+// (64 tokens: 7.8 us instead of 6.8, 5.7 instead of 5.5).
 template <int D>
 constexpr int kFewGroups = D == 64 ? 512 : 256;
 constexpr int kShareFrom = 65;
