@@ -101,7 +101,7 @@ __device__ __forceinline__ void dma(const void *base, const uint32_t (&offset)[N
     else if constexpr (N == 2)
         asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
                      "global_load_lds_dwordx4 %2, %4\n\t"
-                     "global_load_lds_dwordx4 %3, %4 offset:1024\n\t"
+                     "global_load_lds_dwordx4 %3, %4 offset:0x400\n\t"
                      "s_mov_b32 m0, %0"
                      : "=&s"(saved)
                      : "s"(lds), "v"(offset[0]), "v"(offset[1]), "s"(base)
@@ -109,9 +109,9 @@ __device__ __forceinline__ void dma(const void *base, const uint32_t (&offset)[N
     else
         asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
                      "global_load_lds_dwordx4 %2, %6\n\t"
-                     "global_load_lds_dwordx4 %3, %6 offset:1024\n\t"
-                     "global_load_lds_dwordx4 %4, %6 offset:2048\n\t"
-                     "global_load_lds_dwordx4 %5, %6 offset:3072\n\t"
+                     "global_load_lds_dwordx4 %3, %6 offset:0x400\n\t"
+                     "global_load_lds_dwordx4 %4, %6 offset:0x800\n\t"
+                     "global_load_lds_dwordx4 %5, %6 offset:0xc00\n\t"
                      "s_mov_b32 m0, %0"
                      : "=&s"(saved)
                      : "s"(lds), "v"(offset[0]), "v"(offset[1]), "v"(offset[2]), "v"(offset[3]), "s"(base)
