@@ -7,8 +7,8 @@
 // no conversion: a tile of 64 tokens is S^T = K Q^T (16 tokens x 64 channels by 64 channels x
 // 16 columns) and O^T = V^T P^T (16 channels x 64 tokens by 64 tokens x 16 columns).  The other operand has
 // to be int8 too, so a query row and a tile's softmax weights are written as int8 digits to the
-// base 256 under one scale: q 30 bits below the row's largest value in 4 digits, weights 23 bits below the
-// largest of their tile in 3.  Sums of digits are exact in int32 (64 * 127 * 128 < 2^21, 128 * 128 * 128 = 2^21).
+// base 256 under one scale: q 30 bits below the row's largest value in 4 digits, weights, each with the scale of its values
+// on it, 23 bits below the largest such product of their tile in 3.  Sums of digits are exact in int32 (64 * 127 * 128 < 2^21, 128 * 128 * 128 = 2^21).
 // Up to 4 query heads share a key head: the 16 columns are 4 heads x 4 digits, one product does for all digits, and
 // the digits of a score meet in two adds inside a quad of lanes, those of the output once, at the end.
 // More heads (WIDE): the 16 columns are heads, and every digit is a product of its own.
@@ -18,9 +18,10 @@
 // the 16 consecutive tokens 16g .. 16g+15: exactly the 16 bytes of the second
 // product's operand that this lane has to supply, and tokens of one page (a page is a multiple of 16).
 //
-// A query row whose tile has maximum mt takes e_j = exp(s_j - mt) <= 1, digits of e_j under
-// the tile's own maximum, and joins the running sums with exp(mt - m): a tile far below the
-// row's maximum keeps its full digits, so a long flat tail beside one large weight is not lost.
+// A query row whose tile has maximum mt takes e_j = exp(s_j - mt) <= 1, digits of e_j * (scale of j's values) under
+// the tile's largest, and joins the running sums with exp(mt - m): a tile far below the
+// row's maximum keeps its full digits, so a long flat tail beside one large weight is not lost; nor are the small values of
+// a page that has the weight, beside the large ones of a page that has none.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -125,7 +126,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
     constexpr int kQ = WIDE ? 4 : 1;  // products of the scores
     constexpr int kP = WIDE ? 3 : 1;  // and of the sums
     constexpr int kRow = D + 4;
-    constexpr float kUnit = 127.0f * 65536.0f;             // a tile's largest weight in units of its lowest digit
+    constexpr float kUnit = 127.0f * 65536.0f;             // a tile's largest product of weight and scale in units of the lowest digit
     constexpr float kMagic = 8388608.0f + 128.0f * 257.0f;  // 2^23 and a bias of 128 on the two lower digits
 
     __shared__ __align__(16) float s_o[kWaves][kHeads][kRow];
@@ -287,19 +288,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
             for (int i = 0; i < 16; ++i) s[i] = quad_sum((float)__float_as_int(s[i]) * sk_t);
         }
         const int seen = vvalid ? len - vt : 0;  // of this lane's 16 tokens (may exceed 16 or be negative)
-        // scales of the four 16-token groups, under the largest
         const float svs = seen > 0 ? sv_t : 0.0f;
-        const float svmax = max_halves(max_rows16(svs));
-        const float ratio = svmax > 0.0f ? svs / svmax * kUnit : 0.0f;
         if (seen < 16) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = i < seen ? s[i] : -INFINITY;
         }
-        float mt = s[0];
+        float own = s[0];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mt = fmaxf(mt, s[i]);
-        mt = max_halves(max_rows16(mt));
+        for (int i = 1; i < 16; ++i) own = fmaxf(own, s[i]);
+        const float mt = max_halves(max_rows16(own));
         const float ref = mt == -INFINITY ? 0.0f : mt;  // a tile of which nothing is seen: all weights 0
+        // a unit of the lowest digit: the tile's largest product of a weight and a scale is kUnit of them (the bound keeps its inverse finite)
+        const float unit = fmaxf(max_halves(max_rows16(__builtin_amdgcn_exp2f(own - ref) * svs)) * (1.0f / kUnit), 0x1p-126f);
+        const float units = 1.0f / unit;
 
         float sum = 0.0f;
         v4i pd[kP];
@@ -311,7 +312,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
                 const float e = __builtin_amdgcn_exp2f(s[4 * w + r] - ref);
                 sum += e;
                 // one fused product and sum rounds to a whole number in the low bits of the mantissa
-                u[r] = __float_as_uint(__builtin_fmaf(e, ratio, kMagic));
+                u[r] = __float_as_uint(__builtin_fmaf(e * svs, units, kMagic));
             }
             if constexpr (WIDE) {
 #pragma unroll
@@ -334,7 +335,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
         }
         m = mn;
         l = __builtin_fmaf(sum, beta, l);
-        const float w = beta * svmax * weight * (1.0f / kUnit);
+        const float w = beta * unit * weight;
 #pragma unroll
         for (int i = 0; i < kDTiles; ++i) {
             v4i acc[kP];

@@ -501,8 +501,9 @@ bitnet_status_t bitnet_rope_append_kv(const void *qkv, int dt, int64_t row_strid
  *     out[b][i] = sum_j softmax_j(scale * q[b][i] . k_j) v_j,   j < lengths[b]
  * with k_j, v_j the values that the codes stand for.  The products run on the int8
  * matrix cores on the codes as they lie: a query row and the softmax weights of 64 positions are
- * taken as sums of int8 digits to the base 256 (q: 30 bits below the row's largest value, weights: 23 bits below
- * the largest of their 64), summed exactly in int32; statistics and sums over blocks are fp32.
+ * taken as sums of int8 digits to the base 256 (q: 30 bits below the row's largest value; weights, each times the
+ * scale of its values: 23 bits below the largest such product of their 64), summed exactly in int32; statistics and
+ * sums over blocks are fp32.
  *   q          device, [batch][q_heads][head_dim], qdt BITNET_DT_BF16 or BITNET_DT_F32, sequences
  *              `q_stride` elements apart; a row with an infinity or a NaN gives a row of NaN
  *   lengths    device, int32 [batch]: tokens in the cache, the current one included; a length

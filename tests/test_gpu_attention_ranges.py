@@ -1,0 +1,95 @@
+"""Attention side on the GPU: caches and inputs whose values lie far apart or are not finite, under bounds that are those of each row."""
+import numpy as np
+import pytest
+
+import attn_bounds as ab
+import attn_oracle as ao
+
+pytestmark = pytest.mark.gpu
+
+
+def _as(x, dtype):
+    """Host array -> (device tensor of dtype, the fp64 values that it holds)."""
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(getattr(torch, dtype))
+    return t.cuda(), t.double().numpy()
+
+
+def _int(a):
+    import torch
+    return torch.from_numpy(np.asarray(a, np.int32)).cuda()
+
+
+def _dev(c):
+    import torch
+    return [torch.from_numpy(a.copy()).cuda() for a in (c.k, c.v, c.ks, c.vs)]
+
+
+def _decode(q, c, table, lengths, out_dtype):
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    out = bn.bitnet_attn_decode(q, *_dev(c), _int(table), _int(lengths), max(lengths), out_dtype=getattr(torch, out_dtype))
+    torch.cuda.synchronize()
+    return out.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ decode: value scales far apart
+@pytest.mark.parametrize("ratio", [1e-9, 1e-6, 1e-4, 1e-2, 1.0, 1e2, 1e3, 1e4, 1e5, 1e6, 1e9, 1e12])
+@pytest.mark.parametrize("hq", [2, 8])  # digits side by side, and one product after the other
+@pytest.mark.parametrize("page", [16, 32])
+def test_decode_page_of_other_value_scale_without_weight(gpu, hq, page, ratio):
+    """One page of a tile has values `ratio` times those of the rest and scores 42 (60 powers of two) lower: its tokens weigh
+    nothing, and the digits of the others' weights must not be measured by it."""
+    rng = np.random.default_rng(int(page + hq))
+    n, dim = 130, 64
+    c = ao.Cache(-(-n // page), 1, dim, page, rng)
+    table = rng.permutation(c.pages)[None, :]
+    c.ks[:], c.vs[:] = 0.02, 0.03
+    c.k[:, :, :, 0] = 100
+    c.k[:, :, :, 1:] //= 8
+    odd = table[0, 1]
+    c.k[odd, :, :, 0] = -68  # 168 codes of channel 0 below the rest
+    c.vs[odd] = 0.03 * ratio
+    q = rng.standard_normal((1, hq, dim)) * 0.3
+    q[..., 0] = 42 / (168 * 0.02 * dim ** -0.5)
+    for dtype in ("float32", "bfloat16"):
+        qd, q64 = _as(q, dtype)
+        fine, worst = ab.decode_fine(_decode(qd, c, table, [n], dtype), q64, c, table, [n], dim ** -0.5, dtype == "bfloat16")
+        assert fine, (dtype, worst)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq", [3, 12])
+def test_decode_value_scales_over_many_orders(gpu, dim, hq):
+    """Every page a value scale of its own, 24 orders of magnitude apart, and scores a few powers of two apart."""
+    rng = np.random.default_rng(dim + hq)
+    c = ao.Cache(60, 1, dim, 16, rng)
+    c.vs[:] = 10.0 ** rng.uniform(-12, 12, c.vs.shape)
+    table = np.stack([rng.permutation(60)[:30] for _ in range(3)])
+    lengths = [480, 33, 100]
+    qd, q64 = _as(rng.standard_normal((3, hq, dim)), "float32")
+    fine, worst = ab.decode_fine(_decode(qd, c, table, lengths, "float32"), q64, c, table, lengths, dim ** -0.5, False)
+    assert fine, worst
+
+
+@pytest.mark.parametrize("hq", [4, 8])
+@pytest.mark.parametrize("tiny", [0.0, 1e-44, 1e-37, 1e-30])
+def test_decode_value_scales_near_zero(gpu, hq, tiny):
+    """All values tiny, and tiny ones with the weight beside larger ones without: a unit of the weights stays a number."""
+    rng = np.random.default_rng(hq)
+    c = ao.Cache(8, 1, 64, 16, rng)
+    table = np.arange(8)[None, :]
+    c.vs[:] = tiny
+    qd, q64 = _as(rng.standard_normal((1, hq, 64)), "float32")
+    want, tol = ab.decode(q64, c, table, [128], 0.125)
+    got = _decode(qd, c, table, [128], "float32")
+    assert np.all(np.abs(got - want) <= tol + 64 * 128 * 2.0 ** -126 * 127)  # under the least unit, 2^-126, half of it a token
+    c.vs[::2] = 1e30
+    c.k[::2, :, :, 0], c.k[1::2, :, :, 0] = -100, 100
+    c.ks[:] = 0.02
+    q = np.zeros((1, hq, 64))
+    q[..., 0] = 60 / (200 * 0.02 * 0.125)  # the pages with large values weigh e^-60 of the others
+    qd, q64 = _as(q, "float32")
+    fine, worst = ab.decode_fine(_decode(qd, c, table, [128], "float32"), q64, c, table, [128], 0.125, False)
+    assert fine, worst
