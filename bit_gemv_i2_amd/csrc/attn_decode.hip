@@ -252,7 +252,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
         const int vt = t * kTile + 16 * g;
         const bool vvalid = exists(now.v);
         const int8_t *vb = p.v + head_of(now.v) * head_bytes + c * p.page + (vt & (p.page - 1));
-        const float sk_t = sk * qunit, sv_t = sv;
+        // A page with a scale that is not finite makes the rows that see it NaN.  Left to the products it need not: an infinity is stored as
+        // a code, whose score may come out as -infinity and weigh nothing, and a maximum drops a NaN.
+        const float sk_t = __builtin_isfinite(sk) && __builtin_isfinite(sv) ? sk * qunit : __uint_as_float(0x7FC00000u), sv_t = sv;
         v4i vf[kDTiles];
 #pragma unroll
         for (int i = 0; i < kDTiles; ++i) vf[i] = load16<STREAM>(vb + 16 * i * p.page);

@@ -437,7 +437,8 @@ bitnet_status_t bitnet_w2a8_gemv_lut(const uint8_t *packed, const float *scales,
  *              end are not read.  An entry outside 0 .. pages - 1 is never followed:
  *              nothing is stored there, and attention sees no token of that page.
  * A page belongs to one sequence while it is appended to; sequences may share pages that
- * are only read.  Scales are finite and >= 0.  slots * page <= 2^30. */
+ * are only read.  Scales are >= 0; one that is not finite (of keys or values) makes NaN of every row of attention
+ * that sees a token of that page and head.  slots * page <= 2^30. */
 typedef struct {
     int8_t *k, *v;
     float *k_scale, *v_scale;
@@ -476,8 +477,7 @@ bitnet_status_t bitnet_rope_table(int64_t positions, int rot, double base, doubl
  *   codes, if their scale grew, become rint(code * (old / new)); a new code is
  *   clamp(rint(x * (1 / scale)), -127, 127).  (fp32, half to even, correctly rounded divisions.)
  *   Codes of positions that no token has yet are left as they are.
- *   A NaN is stored as code -127; an infinity makes its page's scale infinite, and outputs of
- *   attention over that page and head are then not finite.
+ *   A NaN is stored as code -127; an infinity makes its page's scale infinite.
  *   qkv      device, [tokens][(q_heads + 2 kv_heads) * head_dim], queries, keys, values;
  *            dt BITNET_DT_BF16 or BITNET_DT_F32; rows `row_stride` elements apart
  *   rope     device, fp32 [rope_rows][rot] (bitnet_rope_table)

@@ -93,3 +93,59 @@ def test_decode_value_scales_near_zero(gpu, hq, tiny):
     qd, q64 = _as(q, "float32")
     fine, worst = ab.decode_fine(_decode(qd, c, table, [128], "float32"), q64, c, table, [128], 0.125, False)
     assert fine, worst
+
+
+# ------------------------------------------------------------------ decode: pages that are not finite
+def _digits_of_one_sign(sign):
+    """A query value below 1 whose four digits to the base 256, 30 bits below 1, are 1, 1, 1 and 64."""
+    return sign * 0x01010140 * 2.0 ** -30
+
+
+@pytest.mark.parametrize("n", [1, 65, 129, 5121])  # the first token of a page; the last of these in a context that is cut
+@pytest.mark.parametrize("hq", [2, 8, 16])  # key heads of 1, 4 and 8 queries
+@pytest.mark.parametrize("part", ["key", "value"])
+def test_decode_an_infinity_alone_in_its_page_is_seen(gpu, part, hq, n):
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(n + hq)
+    hk, dim = 2, 64
+    pages = -(-n // 64)
+    table = _int([list(range(pages))])
+    for bad in (np.inf, -np.inf):
+        for sign in (1, -1):
+            c = bn.KVCache.empty(pages, hk, dim, 64)
+            x = rng.uniform(-0.9, 0.9, (n, hq + 2 * hk, dim)).astype(np.float32)
+            x[0, :, 3] = 0.95  # so that the digits of a query lie where they are wanted
+            x[0, :hq, 7] = _digits_of_one_sign(sign)
+            x[n - 1, hq + 1 + (hk if part == "value" else 0), 7] = bad  # of key head 1
+            q, _ = c.append(torch.from_numpy(x).cuda().flatten(1), None, table, _int([0, n]), _int([0]), n, hq)
+            out = c.attend(q[:1].contiguous(), table, _int([n]), n)
+            torch.cuda.synchronize()
+            assert bool(torch.isfinite(out[0, : hq // 2]).all()) and bool(torch.isnan(out[0, hq // 2:]).all()), (bad, sign)
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_decode_scales_that_are_not_finite(gpu, which, bad, page, hq):
+    """NaN for the rows whose length reaches the page, and for the key head that it belongs to; the others as if it were not there."""
+    rng = np.random.default_rng(page + hq)
+    dim, hk = 64, 2
+    lengths = [3 * page, 3 * page + 1, 4 * page, 700, 1]
+    slots = -(-700 // page)
+    c = ao.Cache(5 * slots, hk, dim, page, rng)
+    table = rng.permutation(c.pages).reshape(5, slots)
+    clean = ao.Cache(1, 1, dim, page)
+    clean.__dict__.update({k: (v.copy() if hasattr(v, "copy") else v) for k, v in c.__dict__.items()})
+    if slots > 3:
+        getattr(c, which)[table[:, 3], 1] = bad
+    qd, q64 = _as(rng.standard_normal((5, hq, dim)), "float32")
+    got = _decode(qd, c, table, lengths, "float32")
+    want, tol = ab.decode(q64, clean, table, lengths, dim ** -0.5)
+    nan = np.zeros(got.shape, bool)
+    for b, n in enumerate(lengths):
+        nan[b, hq // 2:] = n > 3 * page
+    assert np.array_equal(np.isnan(got), nan)
+    assert np.all(np.abs(got - want)[~nan] <= tol[~nan])
