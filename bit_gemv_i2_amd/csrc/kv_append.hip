@@ -77,6 +77,11 @@ __device__ __forceinline__ void turn(float a[8], float b[8], const float c[8], c
     }
 }
 
+// Largest magnitudes are compared as the bits of the numbers without their sign, in whose order a NaN is above everything: the float
+// maximum would drop it, and with it every trace of it in the page.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
 __device__ __forceinline__ int code_of(float x, float inv) {
     return (int)fminf(fmaxf(__builtin_rintf(x * inv), -127.0f), 127.0f);
 }
@@ -97,7 +102,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     constexpr int kRows = kThreads / kItems;  // tokens of one pass
     constexpr int kPass = PAGE / kRows;
     constexpr int kVRow = PAGE + 16;
-    __shared__ float s_max[4];
+    __shared__ uint32_t s_max[4];
     __shared__ __align__(16) int8_t s_v[D * kVRow];
 
     const int b = blockIdx.z, unit = blockIdx.y, tid = threadIdx.x;
@@ -157,7 +162,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     const float old = pid >= 0 && r0 > 0 ? *scale : 0.0f;
 
     float a[kPass][8], bb[kPass][8];
-    float most = 0.0f;
+    uint32_t most = 0;
     const T *x = qkv + (p.q_heads + (is_k ? 0 : p.kv_heads) + h) * D;
 #pragma unroll
     for (int i = 0; i < kPass; ++i) {
@@ -182,20 +187,20 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
                 store8(y + ch.b, bb[i]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaxf(fabsf(a[i][e]), fabsf(bb[i][e])));
+            for (int e = 0; e < 8; ++e) most = umax(most, umax(magnitude(a[i][e]), magnitude(bb[i][e])));
         }
     }
     if (pid < 0) return;  // no page: nothing is stored (uniform over the workgroup)
 
     // the page's scale
 #pragma unroll
-    for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+    for (int o = 32; o; o >>= 1) most = umax(most, __shfl_xor(most, o));
     if ((tid & 63) == 0) s_max[tid >> 6] = most;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) most = fmaxf(most, s_max[i]);
-    const float want = fmaxf(most, 1e-5f) / 127.0f;
-    const float now = fmaxf(old, want);
+    for (int i = 0; i < kThreads / 64; ++i) most = umax(most, s_max[i]);
+    const float want = __uint_as_float(umax(most, __float_as_uint(1e-5f))) / 127.0f;
+    const float now = __uint_as_float(umax(magnitude(old), magnitude(want)));  // NaN stays NaN until the page begins anew
     const float inv = 1.0f / now;
     if (tid == 0) *scale = now;
 

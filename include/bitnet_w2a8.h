@@ -477,7 +477,8 @@ bitnet_status_t bitnet_rope_table(int64_t positions, int rot, double base, doubl
  *   codes, if their scale grew, become rint(code * (old / new)); a new code is
  *   clamp(rint(x * (1 / scale)), -127, 127).  (fp32, half to even, correctly rounded divisions.)
  *   Codes of positions that no token has yet are left as they are.
- *   A NaN is stored as code -127; an infinity makes its page's scale infinite.
+ *   An infinity makes its page's scale infinite, a NaN (also one that the turn makes of an infinity) makes it NaN; it stays so
+ *   until a token is written to the page's first position again.  Codes under such a scale are of no meaning.
  *   qkv      device, [tokens][(q_heads + 2 kv_heads) * head_dim], queries, keys, values;
  *            dt BITNET_DT_BF16 or BITNET_DT_F32; rows `row_stride` elements apart
  *   rope     device, fp32 [rope_rows][rot] (bitnet_rope_table)

@@ -149,3 +149,74 @@ def test_decode_scales_that_are_not_finite(gpu, which, bad, page, hq):
         nan[b, hq // 2:] = n > 3 * page
     assert np.array_equal(np.isnan(got), nan)
     assert np.all(np.abs(got - want)[~nan] <= tol[~nan])
+
+
+# ------------------------------------------------------------------ append: values that are not finite
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("dim,page,rot", [(64, 16, 64), (64, 64, 0), (128, 16, 64), (128, 128, 128)])
+@pytest.mark.parametrize("bad", [np.nan, -np.nan, np.inf])
+def test_append_of_values_that_are_not_finite_shows_in_the_scale(gpu, bad, dim, page, rot, dtype):
+    """Scale of the value's page and head not finite, everything else bit for bit; it stays so while the page is appended to, and ends
+    when the page begins anew."""
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(dim + page)
+    hq, hk, n = 4, 2, 3 * page + 7
+    rope = bn.bitnet_rope_table(5 * page, rot) if rot else None
+    x = torch.from_numpy(rng.standard_normal((n + 1, hq + 2 * hk, dim)).astype(np.float32)).to(getattr(torch, dtype))
+    clean = x.float().numpy()
+    for where, head, part in ((0, 0, "k"), (page + 3, 1, "v"), (n - 1, 1, "k"), (n - 1, 0, "v")):
+        for before in (0, 5):
+            c = ao.Cache(6, hk, dim, page, np.random.default_rng(1))
+            dev = _dev(c)
+            table = np.array([[3, 0, 5, 1, 2]])
+            y = x.clone()
+            y[where, hq + head + (hk if part == "v" else 0), dim - 3] = bad
+
+            def append(t, at):
+                bn.bitnet_rope_append_kv(t.cuda().flatten(1), None if rope is None else torch.from_numpy(rope).cuda(), *dev,
+                                         _int(table), _int([0, len(t)]), _int([at]), len(t), hq)
+            append(y[:n], before)
+            c.append(clean[:n], rope, rot, False, table, [0, n], [before], n, hq)
+            slot = (before + where) // page
+            pid = table[0, slot]
+            scales = dev[2] if part == "k" else dev[3]
+            not_finite = np.isnan if np.isnan(bad) else lambda f: not np.isfinite(f)  # (the turn can make a NaN of an infinity)
+            assert not_finite(scales.cpu().numpy()[pid, head])
+            for t, want, touched in zip(dev, (c.k, c.v, c.ks, c.vs), (part == "k", part == "v") * 2):
+                t = t.cpu().numpy()
+                if touched:
+                    t[pid, head] = want[pid, head]
+                assert np.array_equal(t, want)
+            # a finite token behind it, in its page: still seen
+            if before + n < (slot + 1) * page:
+                append(x[n:], before + n)
+                assert not_finite(scales.cpu().numpy()[pid, head])
+            # the page of other tokens: forgotten
+            append(x[:page], slot * page)
+            torch.cuda.synchronize()
+            assert np.isfinite(scales.cpu().numpy()[pid, head])
+
+
+@pytest.mark.parametrize("group", [1, 8])
+@pytest.mark.parametrize("part", ["key", "value"])
+def test_a_nan_that_was_appended_is_seen(gpu, part, group):
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(34)
+    hk, hq, dim, n = 2, 2 * group, 64, 200
+    for dtype in (torch.float32, torch.bfloat16):
+        c = bn.KVCache.empty(4, hk, dim, 64)
+        x = torch.from_numpy(rng.standard_normal((n, hq + 2 * hk, dim)).astype(np.float32)).to(dtype).cuda()
+        x[130, hq + 1 + (hk if part == "value" else 0), 7] = float("nan")  # of key head 1
+        table = _int([[0, 1, 2, 3]])
+        q, _ = c.append(x.flatten(1), None, table, _int([0, n]), _int([0]), n, hq)
+        for length in (n, 129):  # beyond its page's first token, and to it
+            out = c.attend(q[:1], table, _int([length]), length)
+            torch.cuda.synchronize()
+            assert bool(torch.isfinite(out[0, :group]).all()) and bool(torch.isnan(out[0, group:]).all())
+        out = c.attend(q[:1], table, _int([128]), 128)
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(out).all())
