@@ -189,7 +189,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
     const uint32_t part_k = lds + part * kPartBytes, part_v = part_k + PARTS * kPartBytes;  // this part's stages
     const uint32_t lds_k = part_k + side * kLoads * 1024, lds_v = part_v + side * kLoads * 1024;
     // Step t of K (V) into its stage.  Past the end the last step again, so that every step counts the same loads; rows past
-    // the end repeat the last one: their weights are 0, their values finite.
+    // the end repeat the last one, with weights of 0.
     const auto issue = [&](int t, const uint16_t *g, int64_t stride, const uint32_t (&offset)[kLoads], uint32_t to) INLINE {
         to += (t & (kStages - 1)) * kTileBytes;
         t = PARTS * t + part < last_step ? PARTS * t + part : last_step;
@@ -378,51 +378,97 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
     for (int i = side * 64 + lane; i < kTileBytes / 16; i += 64 * kRowWaves) ((lds_v4u *)(uintptr_t)(part_v + 3 * kTileBytes))[i] = v4u{0, 0, 0, 0};
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 
-    bool odd = false;  // the wave's last step has values that are infinite or NaN
-    const auto step = [&](int j, int u) INLINE {  // u = j % 4, a constant
+    // The wave's own steps, j % 4 a constant in each of the four.
+    const auto step = [&](int j, int u) INLINE {
         wait_loads_barrier<3 * kLoads>();
         if (j < quick) {
             issue_next(u);
-        } else if (j < steps) {
+        } else {
             issue_k(j + 4);
             issue_v(j + 2);
         }
-        if (j < wave_steps) {
-            if (u & 1)
-                body(j, u, s1, s0, p1, p0);
-            else
-                body(j, u, s0, s1, p0, p1);
-        } else if (j == wave_steps && j > 0) {  // the last step's second product
-            uint32_t (&pp)[8] = u & 1 ? p0 : p1;
-            v2u16 most = {0, 0};
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < kD; ++i) {
-                    const v4u w = {pp[4 * s], pp[4 * s + 1], pp[4 * s + 2], pp[4 * s + 3]};
-                    const v8bf f = read_v((u + 3) & 3, s, i);
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, __builtin_bit_cast(v8bf, w), o[i], 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        most = __builtin_elementwise_max(most, __builtin_bit_cast(v2u16, __builtin_bit_cast(v4u, f)[e] & 0x7FFF7FFFu));
-                }
-            odd = __any(most[0] >= 0x7F80 || most[1] >= 0x7F80);
-            __builtin_amdgcn_sched_barrier(0);  // the reads are done with before the next barrier gives their stage away
-        }
+        if (u & 1)
+            body(j, u, s1, s0, p1, p0);
+        else
+            body(j, u, s0, s1, p0, p1);
     };
-    for (int j = 0; j <= steps; j += 4) {
+    for (int j = 0; j < wave_steps; j += 4) {
         step(j, 0);
-        if (j + 1 <= steps) step(j + 1, 1);
-        if (j + 2 <= steps) step(j + 2, 2);
-        if (j + 3 <= steps) step(j + 3, 3);
+        if (j + 1 < wave_steps) step(j + 1, 1);
+        if (j + 2 < wave_steps) step(j + 2, 2);
+        if (j + 3 < wave_steps) step(j + 3, 3);
+    }
+    // What is left: the last step's second product, and the loads that other waves wait for.
+    for (int j = wave_steps; j <= steps; ++j) {
+        wait_loads_barrier<3 * kLoads>();
+        if (j < steps) {
+            issue_k(j + 4);
+            issue_v(j + 2);
+        }
+        if (j > wave_steps || j == 0) continue;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = p0[i], b = p1[i];  // (a choice between the arrays themselves would put them into memory)
+            w[i] = j & 1 ? a : b;
+        }
+        v4u f[2 * kD];
+        v2u16 most = {0, 0};
+#pragma unroll
+        for (int x = 0; x < 2 * kD; ++x) {
+            f[x] = __builtin_bit_cast(v4u, read_v((j + 3) & 3, x / kD, x % kD));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = __builtin_elementwise_max(most, __builtin_bit_cast(v2u16, f[x][e] & 0x7FFF7FFFu));
+        }
+        // This step has keys that some of its rows do not see.  Their weight is 0, which hides a finite value only, so values that are not
+        // finite are taken as 0 here and added to the rows that see them, a key at a time.  (8192 tokens, 20 / 5 heads
+        // of 128: 330 us; with an infinity in the last key 380, with NaN throughout 820.)
+        const bool odd = __any(most[0] >= 0x7F80 || most[1] >= 0x7F80);
+        if (odd) {
+#pragma unroll
+            for (int x = 0; x < 2 * kD; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f[x][e] &= ((f[x][e] & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((f[x][e] & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int x = 0; x < 2 * kD; ++x) {
+            const v4u y = {w[4 * (x / kD)], w[4 * (x / kD) + 1], w[4 * (x / kD) + 2], w[4 * (x / kD) + 3]};
+            o[x % kD] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, f[x]), __builtin_bit_cast(v8bf, y), o[x % kD], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // the reads are done with before the next barrier gives their stage away
+        if (!odd) continue;
+        const int key0 = kKeys * (PARTS * (j - 1) + part);
+#pragma unroll 1
+        for (int u = 0; u < kKeys && key0 + u < n; ++u) {
+            const uint16_t *vr = vg + (key0 + u) * p.v_stride;
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) bad |= (vr[64 * i + lane] & 0x7F80) == 0x7F80;
+            if (!__any(bad)) continue;
+            uint32_t word = 0;  // the pair of weights that holds key u's; half-wave (u / 4) % 2 has it
+#pragma unroll
+            for (int i = 0; i < 8; ++i) word = i == 2 * (u >> 3) + ((u >> 1) & 1) ? w[i] : word;
+            word = __shfl(word, col + 8 * (u & 4));
+            const float weight = __uint_as_float(u & 1 ? word & 0xFFFF0000u : word << 16);
+            const bool sees = !p.causal || row >= key0 + u;
+#pragma unroll
+            for (int i = 0; i < kD; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; r += 2) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(vr + 32 * i + 8 * (r / 4) + 4 * half + r % 4);
+                    if (sees && (v & 0x7F80u) == 0x7F80u) o[i][r] = __builtin_fmaf(weight, __uint_as_float(v << 16), o[i][r]);
+                    if (sees && (v & 0x7F800000u) == 0x7F800000u) o[i][r + 1] = __builtin_fmaf(weight, __uint_as_float(v & 0xFFFF0000u), o[i][r + 1]);
+                }
+        }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the end still write to LDS
 
     l = add_halves(l);
     if constexpr (PARTS == 2) {  // join the parts; the stages are free once every wave's loads are done
-        static_assert(kRowWaves * (D / 2 + 3) * 256 <= 2 * PARTS * kPartBytes, "a part's sums fit the stages");
+        static_assert(kRowWaves * (D / 2 + 2) * 256 <= 2 * PARTS * kPartBytes, "a part's sums fit the stages");
         __syncthreads();
-        lds_float *sums = (lds_float *)(uintptr_t)lds + side * ((D / 2 + 3) * 64) + lane, *ml = sums + D / 2 * 64;
+        lds_float *sums = (lds_float *)(uintptr_t)lds + side * ((D / 2 + 2) * 64) + lane, *ml = sums + D / 2 * 64;
         if (part == 1) {
 #pragma unroll
             for (int i = 0; i < kD; ++i)
@@ -430,11 +476,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
                 for (int r = 0; r < 16; ++r) sums[(16 * i + r) * 64] = o[i][r];
             ml[0] = m;
             ml[64] = l;
-            ml[128] = odd ? 1.0f : 0.0f;
         }
         __syncthreads();
         if (part == 1) return;
-        odd |= __any(ml[128] != 0.0f);
         const float m1 = ml[0], mm = fmaxf(m, m1);  // a row sees key 0, in part 0: finite where row < n
         const float a0 = __builtin_amdgcn_exp2f(m - mm), a1 = __builtin_amdgcn_exp2f(m1 - mm);
         l = l * a0 + ml[64] * a1;
@@ -442,43 +486,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         for (int i = 0; i < kD; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[i][r] = o[i][r] * a0 + sums[(16 * i + r) * 64] * a1;
-    }
-    // The last step has keys that some of its rows do not see.  Their weight is 0, which hides a finite value only: if there are others
-    // among them, these rows are taken again one by one.  (Seldom and slow: a lane a key, then a lane a channel.)
-    if (odd) {
-        for (int r = w0; r < w0 + kRowsWave && r < n; ++r) {
-            const uint16_t *qr = p.q + (n0 + r) * p.q_stride + (int64_t)head * D;
-            const int keys = p.causal ? r + 1 : n;
-            const auto score = [&](int key) {
-                float s = 0.0f;
-                for (int c = 0; c < D; c += 8) {
-                    float a[8], b[8];
-                    load8(qr + c, a);
-                    load8(kg + key * p.k_stride + c, b);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(a[e], b[e], s);
-                }
-                return s * p.scale2;
-            };
-            float top = -INFINITY, sum = 0.0f, out[D / 64] = {};
-            for (int key = lane; key < keys; key += 64) top = fmaxf(top, score(key));
-            for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-            for (int first = 0; first < keys; first += 64) {
-                const float e = first + lane < keys ? __builtin_amdgcn_exp2f(score(first + lane) - top) : 0.0f;
-                sum += e;
-                for (int x = 0; x < 64 && first + x < keys; ++x) {
-                    const float weight = __shfl(e, x);
-#pragma unroll
-                    for (int i = 0; i < D / 64; ++i)
-                        out[i] = __builtin_fmaf(weight, __uint_as_float((uint32_t)vg[(first + x) * p.v_stride + 64 * i + lane] << 16), out[i]);
-                }
-            }
-            for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-                p.out[((n0 + r) * p.q_heads + head) * D + 64 * i + lane] = (uint16_t)bf16_pair(out[i] / sum, 0.0f);
-        }
-        return;
     }
     if (row >= n) return;
     const float inv = 1.0f / l;

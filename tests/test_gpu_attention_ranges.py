@@ -220,3 +220,50 @@ def test_a_nan_that_was_appended_is_seen(gpu, part, group):
         out = c.attend(q[:1], table, _int([128]), 128)
         torch.cuda.synchronize()
         assert bool(torch.isfinite(out).all())
+
+
+# ------------------------------------------------------------------ prompt: values and scores that are not finite
+@pytest.mark.parametrize("hq,hk", [(2, 1), (40, 40)])  # keys shared between halves of the waves, and not
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_values_that_are_not_finite_change_nothing_else(gpu, hq, hk, dim, causal):
+    """Infinities and NaN in some channels of some keys: every other channel, and (causal) every row in front of them, to the last bit as
+    without them, whether their key is among the last that a row's wave looks at or not."""
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(40)
+    lens = [300, 70, 1030 if hq == 40 else 97, 33]
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = (_as(rng.standard_normal((int(starts[-1]), h, dim)), "bfloat16")[0] for h in (hq, hk, hk))
+    places = [(0, 0, 1, np.inf), (0, 170, 3, np.inf), (0, 299, 9, -np.inf), (0, 288, dim - 1, np.nan), (1, 69, 5, np.nan), (1, 40, 60, -np.inf),
+              (1, 64, 17, np.inf), (2, 95, 0, np.inf), (2, 96, 33, -np.inf), (3, 32, 62, np.inf)]
+    want = bn.bitnet_attn_prompt(q, k, v, _int(starts), max(lens), causal=causal).clone()
+    odd = torch.zeros(want.shape, dtype=torch.bool, device="cuda")
+    group = hq // hk
+    for b, u, ch, x in places:
+        v[starts[b] + u, hk - 1, ch] = x
+        rows = slice(int(starts[b] + u if causal else starts[b]), int(starts[b + 1]))
+        odd[rows, hq - group:, ch] = True
+        want[rows, hq - group:, ch] = x  # one such value a channel and sequence, and weights above 0
+    got = bn.bitnet_attn_prompt(q, k, v, _int(starts), max(lens), causal=causal)
+    torch.cuda.synchronize()
+    assert torch.equal(got[~odd], want[~odd])
+    assert torch.equal(got[odd].isnan(), want[odd].isnan())
+    assert torch.equal(got[odd].nan_to_num(0.5), want[odd].nan_to_num(0.5))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_of_nan_throughout(gpu, dim, causal):
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    lens = [65, 700, 1]
+    q = torch.ones((sum(lens), 4, dim), dtype=torch.bfloat16, device="cuda")
+    k, nan = q[:, :2].contiguous(), torch.full_like(q[:, :2], float("nan"))
+    starts = _int(np.concatenate([[0], np.cumsum(lens)]))
+    for a in ((q, k, nan), (q, nan, k), (q * float("nan"), k, k)):
+        out = bn.bitnet_attn_prompt(*a, starts, 700, causal=causal)
+        torch.cuda.synchronize()
+        assert bool(out.isnan().all())
