@@ -49,6 +49,9 @@ constexpr int kRowsWave = 32;                 // query rows of a wave
 constexpr int kKeys = 32;                     // keys of a step
 constexpr int kStages = 4;                    // steps of K and of V in LDS
 constexpr float kSlack = 8.0f;                // log2 of the largest weight before a row's reference moves
+// The lowest reference.  Weights are exp2 of a score less the rounded reference, so all of a row are off by the same 2^(half a unit in its
+// last place): nothing for the row, as long as that is a number.
+constexpr float kLowest = -0x1p30f;
 // A launch of at most so many workgroups shares the keys of each between two halves of its waves, which doubles the workgroups: up
 // to where these no longer run at once.  20 heads of 128, one prompt: 512 tokens 12.4 us instead of 16.1, 1536 (240 workgroups)
 // 31.1 instead of 34.2, but 2048 (320) 51.0 instead of 46.8; 32 heads of 64: 512 tokens 9.3 instead of 12.7, 1536 (384) 25.4
@@ -343,7 +346,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         // whole number, so that the scaling is by a power of two and leaves the digits of weights already rounded.
         const float t = max_halves(mx) * p.scale2;
         if (__any(t > m + kSlack)) {
-            const float mn = t > m + kSlack ? m + __builtin_ceilf(t - m) : m;
+            // (from further below than any weight reaches it moves to the score itself, as the scaling is by 0)
+            const float mn = t > m + kSlack ? (t - m < 256.0f ? m + __builtin_ceilf(t - m) : t) : m;
             const float alpha = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= alpha;
@@ -368,7 +372,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         float t = s0[0];
 #pragma unroll
         for (int r = 1; r < 16; ++r) t = fmaxf(t, s0[r]);
-        m = max_halves(t) * p.scale2;  // finite: every row sees key 0
+        // Not below kLowest, also where all these scores are minus infinity: their weights are then 0, and the first score above it takes over.
+        m = fmaxf(max_halves(t) * p.scale2, kLowest);
 #pragma unroll
         for (int i = 0; i < 8; ++i) p1[i] = 0;  // no step before the first
 #pragma unroll
@@ -479,7 +484,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
         }
         __syncthreads();
         if (part == 1) return;
-        const float m1 = ml[0], mm = fmaxf(m, m1);  // a row sees key 0, in part 0: finite where row < n
+        const float m1 = ml[0], mm = fmaxf(m, m1);  // a row sees key 0, in part 0: above minus infinity where row < n
         const float a0 = __builtin_amdgcn_exp2f(m - mm), a1 = __builtin_amdgcn_exp2f(m1 - mm);
         l = l * a0 + ml[64] * a1;
 #pragma unroll

@@ -524,7 +524,8 @@ bitnet_status_t bitnet_attn_decode(const void *q, int qdt, int64_t q_stride, con
  *     out[t][i] = sum_u softmax_u(scale * q[t][i] . k[u]) v[u]
  * over the u of the same sequence, u <= t when causal (infinities and NaN at other u do not matter).  bf16 in and out; scores, softmax
  * statistics and sums are fp32, the weights are rounded to bf16 for the matrix cores (their
- * sum is taken before that rounding).
+ * sum is taken before that rounding).  Scores (times log2 e) are within 2^30: one below that, minus infinity among them, is
+ * taken as a weight of 0, and a row that sees no other is NaN.
  *   q        device, bf16 [tokens][q_heads][head_dim], tokens q_stride elements apart
  *   k, v     device, bf16 [tokens][kv_heads][head_dim], tokens k_stride / v_stride elements
  *            apart (views of a fused projection are read in place)

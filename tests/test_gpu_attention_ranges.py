@@ -267,3 +267,65 @@ def test_prompt_of_nan_throughout(gpu, dim, causal):
         out = bn.bitnet_attn_prompt(*a, starts, 700, causal=causal)
         torch.cuda.synchronize()
         assert bool(out.isnan().all())
+
+
+@pytest.mark.parametrize("hq,hk", [(2, 1), (40, 40)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("masked", [1, 31, 32, 33, 64, 96, 200])
+def test_prompt_keys_whose_scores_are_minus_infinity(gpu, hq, hk, dim, causal, masked):
+    """The first keys of a prompt masked by an infinity in a channel that all queries have above 0: they weigh nothing, and rows that see no
+    others are NaN, as 0 / 0 is."""
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(masked + dim)
+    lens = [300, 70, 1030 if hq == 40 else 230]
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = (rng.standard_normal((int(starts[-1]), h, dim)) for h in (hq, hk, hk))
+    q[..., 5] = np.abs(q[..., 5]) + 0.1
+    (qd, q), (kd, k), (vd, v) = (_as(a, "bfloat16") for a in (q, k, v))
+    for b in range(3):
+        kd[starts[b]: min(starts[b] + masked, starts[b + 1]), :, 5] = -np.inf
+    got = bn.bitnet_attn_prompt(qd, kd, vd, _int(starts), max(lens), causal=causal)
+    torch.cuda.synchronize()
+    got = got.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        rows = slice(starts[b], starts[b + 1])
+        hidden = min(masked, n)
+        see = (np.tril(np.ones((n, n), bool)) if causal else np.ones((n, n), bool)) & (np.arange(n) >= hidden)
+        none = ~see.any(1)
+        assert np.isnan(got[rows][none]).all()
+        for h in range(hq):
+            kk, vv = k[rows, h * hk // hq], v[rows, h * hk // hq]
+            want, a, _ = ao.softmax_rows(q[rows, h], kk, vv, dim ** -0.5, see)
+            tol = 2.0 ** -8 * a + 2.0 ** -15 * np.abs(vv).max()  # as attn_oracle.prompt derives it
+            fine, worst = ao.within(got[rows, h][~none], want[~none], tol[~none], True)
+            assert fine, (b, h, worst)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens", [[100], [100] * 40])
+def test_prompt_scores_that_rise_far(gpu, dim, lens):
+    """Scores of about -2e38 in the first 64 keys, 0 in the next, 2^20 in the last: each outweighs all before it."""
+    import torch
+
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(dim)
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    T, n = int(starts[-1]), lens[0]
+    q, k = np.zeros((T, 8, dim)), np.zeros((T, 8, dim))
+    q[..., 0] = 2.0 ** 63
+    at = np.arange(T) % n
+    k[at < 64, :, 0] = -(2.0 ** 64)
+    k[at == n - 1, :, 0] = 2.0 ** -43
+    (qd, _), (kd, _), (vd, v) = (_as(a, "bfloat16") for a in (q, k, rng.standard_normal((T, 8, dim))))
+    got = bn.bitnet_attn_prompt(qd, kd, vd, _int(starts), n, scale=1.0)
+    torch.cuda.synchronize()
+    got = got.double().cpu().numpy()
+    for s in starts[:-1]:
+        for row, first in ((64, 64), (90, 64), (n - 1, n - 1)):
+            x = v[s + first: s + row + 1]
+            want, a = x.mean(0), np.abs(x).mean(0)
+            fine, worst = ao.within(got[s + row], want, 2.0 ** -8 * a + 2.0 ** -15 * np.abs(v).max(), True)
+            assert fine, (row, worst)
