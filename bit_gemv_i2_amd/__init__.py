@@ -546,6 +546,8 @@ def bitnet_w2a8_gemv_lut(packed, scales, q, s_a, N: int, K: int, tiles_per_group
 
 # ------------------------------------------------------------------ attention side of a decoder layer
 def bitnet_kv_cache_bytes(pages: int, kv_heads: int, head_dim: int, page: int) -> int:
+    for n, name in ((kv_heads, "kv_heads"), (head_dim, "head_dim"), (page, "page")):
+        _bound(n, name)
     return lib().bitnet_kv_cache_bytes(int(pages), int(kv_heads), int(head_dim), int(page))
 
 
@@ -554,6 +556,10 @@ def bitnet_rope_table(positions: int, rot: int, base: float = 10000.0, factor: f
     positions: all rates by 1/factor, or by parts when `trained` gives the context length of the training."""
     if positions < 1 or rot < 1:
         raise BitnetError(BITNET_ERR_UNSUPPORTED_SHAPE, "bitnet_rope_table")
+    _bound(positions, "positions")
+    _bound(rot, "rot")
+    if not -1 << 63 <= trained < 1 << 63:
+        raise ValueError("trained must be below 2^63")
     t = np.empty((positions, rot), np.float32)
     _ok(lib().bitnet_rope_table(int(positions), int(rot), float(base), float(factor), int(trained), _np_ptr(t)),
         "bitnet_rope_table")
@@ -652,8 +658,8 @@ def _empty(torch, like, shape, dtype, stream):
 
 def _bound(n: int, name: str):
     """ctypes would cut a count to its low 32 bits without a word."""
-    if n > 0x7FFFFFFF:
-        raise ValueError(f"{name} must be below 2^31")
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
+        raise ValueError(f"{name} must be below 2^31 and not below -2^31")
 
 
 def _float_dt(torch, t, name: str) -> int:
@@ -706,7 +712,8 @@ def bitnet_rope_append_kv(qkv, rope, k_cache, v_cache, k_scale, v_scale, table, 
 
 
 def bitnet_attn_decode_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int) -> int:
-    _bound(max_len, "max_len")
+    for n, name in ((batch, "batch"), (q_heads, "q_heads"), (kv_heads, "kv_heads"), (head_dim, "head_dim"), (max_len, "max_len")):
+        _bound(n, name)
     return lib().bitnet_attn_decode_workspace_bytes(int(batch), int(q_heads), int(kv_heads), int(head_dim),
                                                     int(max_len))
 
