@@ -621,9 +621,11 @@ def _on_device(t, name: str, dev: int, dtype=None, shape=None):
 
 
 def _launch_stream(torch, stream, dev: int):
-    """The stream handle of a launch on device `dev`, which has to be the current one."""
+    """The stream handle of a launch on device `dev`, which has to be the current one and the stream's."""
     if torch._C._cuda_getDevice() != dev:
-        raise ValueError(f"the tensors are on device {dev}, the current device is {torch.cuda.current_device()}")
+        raise ValueError(f"the tensors are on device {dev}, the current device is {torch._C._cuda_getDevice()}")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the tensors are on device {dev}, the stream is of device {stream.device.index}")
     # the handle alone: current_stream() builds an object around it, for as long as a launch takes
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 

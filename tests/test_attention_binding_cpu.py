@@ -44,3 +44,19 @@ def test_sizes_outside_32_bits(n):
 def test_negative_counts_inside_32_bits_are_refused_by_the_library():
     assert bn.bitnet_kv_cache_bytes(4, -2, 64, 16) == 0
     assert bn.bitnet_attn_decode_workspace_bytes(3, 4, 2, 64, -(1 << 31)) == 0
+
+
+def test_a_launch_stream_is_of_the_tensors_device(monkeypatch):
+    """A launch on another device's stream would run there, on addresses of this one."""
+    import types
+
+    import torch
+
+    def stream(index):
+        return types.SimpleNamespace(device=torch.device("cuda", index), cuda_stream=0x1234)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    assert bn._launch_stream(torch, stream(1), 1) == 0x1234
+    with pytest.raises(ValueError, match="the stream is of device 0"):
+        bn._launch_stream(torch, stream(0), 1)
+    with pytest.raises(ValueError, match="the current device is 1"):
+        bn._launch_stream(torch, stream(0), 0)
