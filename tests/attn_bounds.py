@@ -45,3 +45,28 @@ def decode_fine(got, q, cache, table, lengths, scale, bf16):
     """(all fine, worst share of the tolerance) of an output against `decode`."""
     want, tol = decode(q, cache, table, lengths, scale)
     return ao.within(got, want, tol, bf16)
+
+
+def emulate(q, cache, table, lengths, scale, q_bits=30, weight_unit=127 * 65536):
+    """Decode attention with the kernel's digits and 64 bits for everything else: queries as whole multiples of 2^-q_bits of the power of two above
+    their row's largest, products of weight and value scale as whole multiples of 1 / weight_unit of the largest of their 64."""
+    B, hq, D = q.shape
+    group = hq // cache.heads
+    out = np.zeros_like(q)
+    for b in range(B):
+        n = max(0, int(lengths[b]))
+        k, v = cache.values(table[b], n)
+        vs = np.repeat(cache.vs[table[b, : -(-n // cache.page)]].astype(np.float64), cache.page, axis=0)[:n]
+        for i in range(hq if n else 0):
+            step = 2.0 ** (np.frexp(np.abs(q[b, i]).max())[1] - q_bits)
+            s = (k[i // group] @ (np.rint(q[b, i] / step) * step)) * scale
+            total, l = np.zeros(D), 0.0
+            for t in range(0, n, TILE):
+                e, sv = np.exp(s[t: t + TILE] - s[t: t + TILE].max()), vs[t: t + TILE, i // group]
+                unit = max((e * sv).max() / weight_unit, 1e-300)
+                codes = np.divide(v[i // group, t: t + TILE], sv[:, None], out=np.zeros((len(sv), D)), where=sv[:, None] > 0)
+                beta = np.exp(s[t: t + TILE].max() - s.max())
+                total += beta * unit * (np.rint(e * sv / unit) @ codes)
+                l += beta * e.sum()
+            out[b, i] = total / l
+    return out

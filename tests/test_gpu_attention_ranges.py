@@ -34,6 +34,39 @@ def _decode(q, c, table, lengths, out_dtype):
     return out.double().cpu().numpy()
 
 
+# ------------------------------------------------------------------ decode: the digits' bounds, whatever the types
+EDGES = [1, 0, 15, 16, 17, 63, 64, 65, 127, 128, 129, 700]
+
+
+@pytest.mark.parametrize("qdt,odt", [("bfloat16", "bfloat16"), ("float32", "float32"), ("bfloat16", "float32"), ("float32", "bfloat16")])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("hq", [2, 8, 20])
+def test_decode_types_within_the_bounds_of_30_and_23_bits(gpu, hq, page, dim, qdt, odt):
+    """Queries have 30 bits and weights 23 in every combination of types."""
+    rng = np.random.default_rng(hq + page + dim)
+    slots = -(-max(EDGES) // page)
+    c = ao.Cache(len(EDGES) * slots, 2, dim, page, rng)
+    table = rng.permutation(c.pages).reshape(len(EDGES), slots)
+    qd, q64 = _as(rng.standard_normal((len(EDGES), hq, dim)) * 1.5, qdt)
+    got = _decode(qd, c, table, EDGES, odt)
+    want, tol = ao.decode(q64, c, table, EDGES, dim ** -0.5, True, 30)
+    fine, worst = ao.within(got, want, tol, odt == "bfloat16")
+    assert fine, worst
+
+
+@pytest.mark.parametrize("qdt,odt", [("bfloat16", "bfloat16"), ("bfloat16", "float32"), ("float32", "bfloat16")])
+@pytest.mark.parametrize("hq,dim,page,n", [(4, 64, 16, 9000), (12, 128, 64, 4000), (1, 128, 128, 20001)])
+def test_decode_types_in_long_contexts(gpu, hq, dim, page, n, qdt, odt):
+    rng = np.random.default_rng(n)
+    c = ao.Cache(-(-n // page), 1, dim, page, rng)
+    table = rng.permutation(c.pages)[None, :]
+    qd, q64 = _as(rng.standard_normal((1, hq, dim)) * 1.5, qdt)
+    want, tol = ao.decode(q64, c, table, [n], dim ** -0.5, True, 30)
+    fine, worst = ao.within(_decode(qd, c, table, [n], odt), want, tol, odt == "bfloat16")
+    assert fine, worst
+
+
 # ------------------------------------------------------------------ decode: value scales far apart
 @pytest.mark.parametrize("ratio", [1e-9, 1e-6, 1e-4, 1e-2, 1.0, 1e2, 1e3, 1e4, 1e5, 1e6, 1e9, 1e12])
 @pytest.mark.parametrize("hq", [2, 8])  # digits side by side, and one product after the other
