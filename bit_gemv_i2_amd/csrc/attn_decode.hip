@@ -40,17 +40,17 @@ namespace {
 // What bounds it: the cache's bytes.  64 x 8192 tokens, 32 / 8 heads of 128: 1.08 GB in 171 us, 6.3 TB/s, 98% of a bare read;
 // one sequence of 131071 tokens, 20 / 5 heads: 168 MB in 35 us (4.8 TB/s) and 4 us to join 98 splits; 16 sequences
 // of up to 4000: 42 MB in 14 us and 4 to join, the chain of a wave's three tiles: 2 us to the first keys
-// (lengths, pages, keys), then 2 to 3 a tile.  A tile takes some 340 VALU operations of a wave, 1400 cycles; a SIMD's share of
+// (lengths, pages, keys), then 2 to 3 a tile.  A tile takes some 360 VALU operations of a wave, 1450 cycles; a SIMD's share of
 // the bandwidth brings one in 5800.
 constexpr int kWaves = 4;       // waves of a workgroup, which take its tiles in turn
 constexpr int kTile = 64;       // tokens of a tile: one int8 product's depth
 // Workgroups that a launch is split into where the contexts allow: 2 for each of 256 CUs, as many as the registers let
-// reside.  (131071 tokens, 20 / 5 heads of 128: 34.9 us, 768 35.4, 1024 37.5, and a longer join.)
+// reside.  (131071 tokens, 20 / 5 heads of 128, with the join: 33.5 us in a graph, 768 34.7, 1024 38.5.)
 constexpr int kWantGroups = 512;
-// Caches of more bytes than the memory-side cache holds are read past it (non-temporal loads): 1.07 GB in 171 us
-// instead of 187, 98% of a bare read's rate; 42 MB, which that cache keeps from call to call, in 14.4 us, but 17.2
+// Caches of more bytes than the memory-side cache holds, going by the bound on the lengths, are read past it (non-temporal loads): 1.07 GB in
+// 172 us instead of 182, 98% of a bare read's rate; 42 MB, which that cache keeps from call to call, in 18.4 us, but 21.2
 // so.  Not for pages of 128: a tile takes half of each 128-byte line of values, and the line has to stay for the
-// other half (1.07 GB: 187 us, but 221 so).
+// other half (1.07 GB: 190 us, but 224 so).
 constexpr int64_t kStreamBytes = 256ll << 20;
 
 struct DecodeArgs {
@@ -445,14 +445,15 @@ __global__ __launch_bounds__(kJoinRuns *D / 4) void attn_join_kernel(DecodeArgs 
 }
 
 // Query heads of one workgroup: the columns of a product, with the digits beside each other or (WIDE) one after the other.
-// Groups of 4 are a little faster narrow (16 sequences of up to 4000 tokens, 20 / 5 heads of 128: 14.1 us, wide 15.2); larger ones
-// would read their keys and values once for every 4 heads (64 x 8192 tokens, 8 key heads of 128: a group of 8 takes 181 us
-// wide and 367 narrow, of 16 184 and 741).
+// Groups of 4 are a little faster narrow (16 sequences of up to 4000 tokens, 20 / 5 heads of 128, in a graph: 16.7 us with the join, wide 17.8); larger
+// ones would read their keys and values once for every 4 heads (64 x 8192 tokens, 8 key heads of 128: a group of 8 takes 188 us
+// wide and 369 narrow, of 16 193 and 743).
 int heads_of(int group) { return group <= 4 ? 4 : 16; }
 
 // Contexts of so few tiles are not cut: a tile more for each wave costs 1.25 us, the join 2.8 and, where the host launches it, a
-// call's other 4.  One sequence, 20 / 5 heads of 128: 768 tokens whole 7.9 us (8.0 cut) in a graph, 10.4 (14.6) called;
-// 1024 tokens 9.0 (8.1) and 10.3 (14.6); 1536 tokens 11.6 (8.2) and 11.7 (14.3).
+// call's other 5.  One sequence, 20 / 5 heads of 128: 768 tokens whole 7.7 us (8.1 cut) in a graph, 10.5 (15.5) called;
+// 1024 tokens 9.0 (8.0) and 10.5 (15.5); 1536 tokens 11.6 (8.1) and 11.6 (15.3).  The limit is the one for calls: between 769 and 1024 tokens a graph
+// would be up to 1 us faster cut, a call 5 us slower.
 constexpr int kWhole = 4 * kWaves;
 
 // Tiles of one workgroup.  The longest contexts are cut so that all workgroups are resident at once

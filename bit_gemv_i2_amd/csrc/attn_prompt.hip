@@ -6,19 +6,24 @@
 // Both products are taken transposed: S^T = K Q^T and O^T = V^T P^T, with
 // v_mfma_f32_32x32x16_bf16.  A lane then holds one query row (lane % 32) and 16 of its scores for
 // 32 keys, the rows 8j + 4 (lane / 32) + r of the result: the softmax needs one exchange between the two
-// half-waves and no other, and a lane's scores, rounded to bf16, are its own operand of the second
+// half-waves and no other, and a lane's weights, rounded to bf16, are its own operand of the second
 // product, if that product takes its 16 keys in the order 8x + 4 (lane / 32) + r.  V^T is read from LDS by
 // the transposing 16-bit read, which gives a lane 4 keys of one channel: that same order.
+//
+// The weights are rounded to 8 bits because the values are bf16 and the matrix cores take two operands of one type; a second bf16 for what the
+// rounding drops would be half as many products again.  Their sum is of the unrounded ones.  Relative error of the bf16 outputs 0.0019 to 0.0021; of
+// rounding the exact ones 0.0016.
 //
 // A wave has 32 rows and runs one software pipeline over steps of 32 keys: beside the 16 products (128 channels) that make
 // the scores of step j + 1 and add step j - 1 to the sums, it turns the scores of step j into weights, one a
 // product.  K and V come by direct loads into a ring of four steps, two to three steps ahead.
 //
-// What bounds it (8192 tokens, 20 / 5 heads of 128, causal: 335 us, 1.03 PFLOP/s, 79% of what the library's largest
-// bf16 product reaches here; 9 prompts of up to 2047 tokens, 32 / 8 heads of 64: 98 us, 0.66 PFLOP/s).  The matrix cores are busy
-// for 60% of the cycles at 128 channels, at a clock that falls from 2.4 to about 1.9 GHz under the load.  A step of one wave
+// What bounds it (8192 tokens, 20 / 5 heads of 128, causal: 326 us, 1.05 PFLOP/s, 83% of a bf16 product of 8192 x 8192 x 8192 by the library,
+// 77% of one of 16384; 9 prompts of up to 2047 tokens, 32 / 8 heads of 64: 94 us, 0.69 PFLOP/s).  The matrix cores are busy
+// for 65% of the cycles at 128 channels, at a clock that falls from 2.4 to about 1.9 GHz under the load.  A step of one wave
 // alone takes some 1400 cycles, 512 of them products: the issue of its 220 instructions, the direct loads (a quarter), the
-// step's end with its reference and barrier.  Two waves a SIMD hide half of that.  Measured and not kept: 64 rows a wave
+// step's end with its reference and barrier.  Two waves a SIMD hide half of that.  A wave's last product stands behind its loop: inside, as a branch
+// of each of the four stages, it cost the loop 45 registers of 250 at 128 channels and 4% of the time.  Measured and not kept: 64 rows a wave
 // (half the LDS reads, but one wave a SIMD: 420 us against 350 at the time), 8 waves sharing a ring (369), operands read 5
 // products ahead (352), the reference checked beside the next step's first products (364), steps of 64 keys at 64 channels (109
 // against 106); wave priorities and all first loads ahead of the queries (no change).
@@ -53,13 +58,14 @@ constexpr float kSlack = 8.0f;                // log2 of the largest weight befo
 // last place): nothing for the row, as long as that is a number.
 constexpr float kLowest = -0x1p30f;
 // A launch of at most so many workgroups shares the keys of each between two halves of its waves, which doubles the workgroups: up
-// to where these no longer run at once.  20 heads of 128, one prompt: 512 tokens 12.4 us instead of 16.1, 1536 (240 workgroups)
-// 31.1 instead of 34.2, but 2048 (320) 51.0 instead of 46.8; 32 heads of 64: 512 tokens 9.3 instead of 12.7, 1536 (384) 25.4
-// instead of 28.4, 2048 (512) 36.1 instead of 37.2, 3000 (768) 65 instead of 58.6.  Two steps are too few to share
-// (64 tokens: 7.8 us instead of 6.8, 5.7 instead of 5.5).
+// to where these no longer run at once.  20 heads of 128, one prompt: 512 tokens 12.1 us instead of 15.3, 1536 (240 workgroups)
+// 29.1 instead of 30.6, but 2048 (320) 46.6 instead of 41.3; 32 heads of 64: 512 tokens 9.4 instead of 12.6, 1536 (384) 24.4
+// instead of 25.9, 2048 (512) 33.9 instead of 33.4, 3000 (768) 56.8 instead of 52.1.  Two steps are too few to share, three are not
+// (20 heads of 128: 33 to 64 tokens 7.8 us instead of 6.7, 65 to 96 8.0 instead of 8.3, 128 8.7 instead of 9.7; 32 heads of 64: 64 tokens 5.9
+// instead of 5.6, 96 5.9 instead of 6.7, 128 6.6 instead of 7.8).
 template <int D>
 constexpr int kFewGroups = D == 64 ? 512 : 256;
-constexpr int kShareFrom = 65;
+constexpr int kShareFrom = 2 * kKeys + 1;
 constexpr int64_t kMaxTokens = 1 << 22;
 constexpr int64_t kMaxTiles = 1u << 30;  // a workgroup's number stays inside 32 bits and the launch's dimensions inside 16
 constexpr int64_t kMaxStride = 1 << 23;  // a lane's offset inside a step stays inside 32 bits
@@ -152,8 +158,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(PromptArgs 
 
     // Workgroups go to the eight dies in turn, each with an L2 of its own.  x is 8 g + die for head g of a group, so that the heads that
     // share keys share an L2, and where batch * kv_heads is a multiple of 8 all row blocks of a sequence do.  Against heads in
-    // turn, 9 prompts of 2047 tokens: 32 / 8 heads of 64 channels 211 us instead of 228 (L2 misses to a quarter), 20 / 5 of 128 232
-    // instead of 260; one prompt of 8192 the same.
+    // turn, 9 prompts of 2047 tokens: 32 / 8 heads of 64 channels 205 us instead of 227 (L2 misses to a quarter), 20 / 5 of 128 217
+    // instead of 250; one prompt of 8192 the same.
     const uint32_t tile = (blockIdx.z * gridDim.y + blockIdx.y) * 8 + blockIdx.x % 8, level = tile / p.units, unit = tile % p.units;
     if (level >= p.blocks) return;
     const int b = unit / p.kv_heads, hk = unit % p.kv_heads, head = hk * (gridDim.x / 8) + blockIdx.x / 8;

@@ -509,6 +509,8 @@ bitnet_status_t bitnet_rope_append_kv(const void *qkv, int dt, int64_t row_strid
  *              `q_stride` elements apart; a row with an infinity or a NaN gives a row of NaN
  *   lengths    device, int32 [batch]: tokens in the cache, the current one included; a length
  *              above max_len or slots * page is read as that, one below 1 gives zeros
+ *   max_len    bounds the lengths.  The launch is shaped by it, as the lengths are on the device (how contexts are cut, whether a cache is
+ *              taken to exceed the memory-side cache): right for any bound, fastest for a close one
  *   out        device, [batch][q_heads][head_dim], odt BITNET_DT_BF16 or BITNET_DT_F32
  *   workspace  device, 256-byte aligned, >= bitnet_attn_decode_workspace_bytes(...); clobbered; may
  *              be NULL where that is 0
