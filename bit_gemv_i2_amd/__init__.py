@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libbitnet_w2a8.so")
 BITNET_OK, BITNET_ERR_INVALID_ARG, BITNET_ERR_UNSUPPORTED_SHAPE, BITNET_ERR_HIP = 0, 1, 2, 3
 BITNET_DT_BF16, BITNET_DT_F32, BITNET_DT_F32_FOLD2, BITNET_DT_F32_RELU2_GLU = 0, 1, 2, 3
 BITNET_JUNCTION_NONE, BITNET_JUNCTION_SUM, BITNET_JUNCTION_RELU2_GLU = 0, 1, 2
+BITNET_ACT_NONE, BITNET_ACT_RELU, BITNET_ACT_RELU2, BITNET_ACT_SILU, BITNET_ACT_GELU = 0, 1, 2, 3, 4
+_ACTS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4}
 _JUNCTIONS = {False: 0, None: 0, "none": 0, True: 1, "sum": 1, "relu2_glu": 2, 0: 0, 1: 1, 2: 2}
 
 
@@ -111,6 +113,17 @@ _SIGS = {
                             ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
     "bitnet_attn_prompt": ([ctypes.c_void_p, ctypes.c_int64] * 3 + [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64]
                            + [ctypes.c_int] * 5 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "bitnet_add_norm": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                         ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_int]
+                        + [ctypes.c_void_p] * 4 + [ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
+    "bitnet_w2a8_linear": ([ctypes.c_void_p] * 5 + [ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]
+                           + [ctypes.c_int] * 4 + [ctypes.c_void_p], ctypes.c_int),
+    "bitnet_w2a8_grouped": ([ctypes.c_void_p] * 4 + [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                             ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p] + [ctypes.c_int] * 3
+                            + [ctypes.c_void_p], ctypes.c_int),
+    "bitnet_route_workspace_bytes": ([ctypes.c_int] * 3, ctypes.c_size_t),
+    "bitnet_route": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int64] + [ctypes.c_int] * 4 + [ctypes.c_void_p] * 6
+                     + [ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
 }
 
 
@@ -785,6 +798,201 @@ def bitnet_attn_prompt(q, k, v, starts, max_len: int, causal: bool = True, scale
     return out
 
 
+# ------------------------------------------------------------------ between the products of a decoder layer
+def _add_norm(name, x, weight, eps, add, slots, gates, x_out, q, s_a, h, h_dtype, stream):
+    """The checks and the launch behind bitnet_add_norm_quant (h_dtype None) and bitnet_add_norm."""
+    torch = _torch or _import_torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [M][K]")
+    M, K = x.shape
+    _bound(M, "M")
+    _bound(K, "K")
+    dev = x.get_device()
+    xp, xdt = _on_device(x, "x", dev), _float_dt(torch, x, "x")
+    ap = adt = sp = gp = rows = parts = 0
+    if slots is not None and add is None or (slots is None) != (gates is None):
+        raise ValueError("slots and gates come together, and with add")
+    if add is not None:
+        ap, adt = _on_device(add, "add", dev), _float_dt(torch, add, "add")
+        if slots is None:
+            if add.shape != x.shape:
+                raise ValueError(f"add must be [{M}][{K}], not {tuple(add.shape)}")
+        else:
+            if add.dim() != 2 or add.shape[1] != K or slots.dim() != 2 or slots.shape[0] != M:
+                raise ValueError(f"with slots [{M}][parts] add must be [rows][{K}]")
+            rows, parts = add.shape[0], slots.shape[1]
+            _bound(parts, "parts")
+            sp = _on_device(slots, "slots", dev, torch.int32)
+            gp = _on_device(gates, "gates", dev, torch.float32, slots.shape)
+        if x_out is None:
+            x_out = _empty(torch, x, (M, K), x.dtype, stream)
+        op = _on_device(x_out, "x_out", dev, x.dtype, x.shape)
+    else:
+        if x_out is not None:
+            raise ValueError("x_out comes with add")
+        x_out, op = x, None
+    wp = None if weight is None else _on_device(weight, "weight", dev, torch.float32, (K,))
+    qp = sap = hp = None
+    hdt = 0
+    if h_dtype is None:
+        if q is None:
+            q = _empty(torch, x, (M, K), torch.int8, stream)
+        if s_a is None:
+            s_a = _empty(torch, x, (M,), torch.float32, stream)
+        qp, sap = _on_device(q, "q", dev, torch.int8, x.shape), _on_device(s_a, "s_a", dev, torch.float32, (M,))
+    else:
+        if h is None:
+            h = _empty(torch, x, (M, K), h_dtype, stream)
+        hp, hdt = _on_device(h, "h", dev, h_dtype, x.shape), _float_dt(torch, h, "h")
+    _ok(lib().bitnet_add_norm(xp, xdt, ap or None, adt, rows, sp or None, gp or None, parts, wp, eps, M, K, op, qp, sap, hp, hdt,
+                              _launch_stream(torch, stream, dev)), name)
+    return q, s_a, h, x_out
+
+
+def bitnet_add_norm_quant(x, weight=None, eps: float = 1e-5, add=None, slots=None, gates=None, x_out=None, q=None, s_a=None,
+                          stream=None):
+    """Residual addition, root-mean-square norm and int8 quantisation: x [M][K] bf16 or fp32, plus add [M][K] (or, with
+    slots int32 [M][parts] and gates fp32 [M][parts], plus the gated sum of those rows of add [rows][K]).  Returns
+    (q int8 [M][K], s_a fp32 [M], the new stream); the last is x itself without add, else x_out (allocated unless given;
+    x serves)."""
+    q, s_a, _, x_out = _add_norm("bitnet_add_norm_quant", x, weight, eps, add, slots, gates, x_out, q, s_a, None, None, stream)
+    return q, s_a, x_out
+
+
+def bitnet_add_norm(x, weight=None, eps: float = 1e-5, add=None, slots=None, gates=None, x_out=None, out_dtype=None, h=None,
+                    stream=None):
+    """bitnet_add_norm_quant without the quantiser, as before a product of other types: returns (h [M][K] in out_dtype,
+    x's by default, and the new stream)."""
+    _, _, h, x_out = _add_norm("bitnet_add_norm", x, weight, eps, add, slots, gates, x_out, None, None, h,
+                               out_dtype or (x.dtype if h is None else h.dtype), stream)
+    return h, x_out
+
+
+def _act_code(act) -> int:
+    try:
+        return _ACTS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown activation {act!r}") from None
+
+
+def _product_ptrs(torch, packed, scales, q, s_a, N, K, matrices):
+    """(device, packed, scales, q, s_a pointers, tokens) of `matrices` weights N x K one behind the other and activations."""
+    dev = q.get_device()
+    pp, sp = _on_device(packed, "packed", dev, torch.uint8), _on_device(scales, "scales", dev, torch.float32)
+    if N < 1 or K < 1 or packed.numel() * 4 != matrices * N * K or scales.numel() * 128 != matrices * N * K:
+        if bitnet_packed_bytes(_i64(N), _i64(K)) == 0:
+            raise BitnetError(BITNET_ERR_UNSUPPORTED_SHAPE, f"weights of shape {N} x {K}")
+        _check(packed, "packed", torch.uint8, numel=matrices * N * K // 4)
+        _check(scales, "scales", torch.float32, numel=matrices * N * K // 128)
+    _bound(N, "N")
+    _bound(K, "K")
+    if q.dim() != 2 or q.shape[1] != K:
+        raise ValueError(f"q must be [M][{K}], not {tuple(q.shape)}")
+    M = q.shape[0]
+    _bound(M, "M")
+    return dev, pp, sp, _on_device(q, "q", dev, torch.int8), _on_device(s_a, "s_a", dev, torch.float32, (M,)), M
+
+
+def _i64(n: int) -> int:
+    if not -1 << 63 <= n < 1 << 63:
+        raise ValueError("a size must be below 2^63")
+    return n
+
+
+def bitnet_w2a8_linear(packed, scales, q, s_a, N: int, K: int, bias=None, act="none", gated: bool = False, residual=None,
+                       out_dtype=None, y=None, stream=None):
+    """W2A8 product with an epilogue, any number of tokens: act(z) + residual, or gated act(z[:, :N/2]) * z[:, N/2:] + residual, with
+    z = product + bias.  act: "none", "relu", "relu2", "silu" or "gelu"; bias fp32 [N]; residual bf16 or fp32 of y's shape (y itself
+    serves).  Returns y [M][N, or N/2 when gated] in out_dtype (y's, else the residual's, else bf16)."""
+    torch = _torch or _import_torch()
+    code = _act_code(act)
+    dev, pp, sp, qp, sap, M = _product_ptrs(torch, packed, scales, q, s_a, N, K, 1)
+    shape = (M, N // 2 if gated else N)
+    bp = None if bias is None else _on_device(bias, "bias", dev, torch.float32, (N,))
+    rp, rdt = None, 0
+    if residual is not None:
+        rp, rdt = _on_device(residual, "residual", dev, None, None), _float_dt(torch, residual, "residual")
+        if residual.shape != shape:
+            raise ValueError(f"residual must be {list(shape)}, not {tuple(residual.shape)}")
+    if y is None:
+        y = _empty(torch, q, shape, out_dtype or (torch.bfloat16 if residual is None else residual.dtype), stream)
+    yp, ydt = _on_device(y, "y", dev, out_dtype, shape), _float_dt(torch, y, "y")
+    _ok(lib().bitnet_w2a8_linear(pp, sp, qp, sap, bp, code, bool(gated), rp, rdt, yp, ydt, M, N, K,
+                                 _launch_stream(torch, stream, dev)), "bitnet_w2a8_linear")
+    return y
+
+
+# ------------------------------------------------------------------ a layer of experts
+def bitnet_route_workspace_bytes(tokens: int, experts: int, k: int) -> int:
+    for n, name in ((tokens, "tokens"), (experts, "experts"), (k, "k")):
+        _bound(n, name)
+    return lib().bitnet_route_workspace_bytes(int(tokens), int(experts), int(k))
+
+
+def bitnet_route(logits, k: int, over_all: bool = False, out=None, workspace=None, stream=None):
+    """The k experts of each token and the plan that sorts tokens by expert: logits [T][E] bf16 or fp32, rows at any stride.
+    Returns (chosen int32 [T][k], gates fp32 [T][k], starts int32 [E + 1], rows int32 [T * k], slots int32 [T][k]); `out` gives
+    these five.  Gates are the softmax of the chosen logits, or with over_all their share of the softmax over all experts."""
+    torch = _torch or _import_torch()
+    _bound(k, "k")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [T][E] with the experts side by side")
+    dt = _float_dt(torch, logits, "logits")
+    T, E = logits.shape
+    _bound(T, "T")
+    _bound(E, "E")
+    dev = logits.get_device()
+    if dev < 0:
+        raise ValueError("logits must be a device tensor")
+    need = bitnet_route_workspace_bytes(T, E, k)
+    shapes = ((T, k), (T, k), (E + 1,), (T * k,), (T, k))
+    if out is None:
+        if T < 1 or not 1 <= k <= E:
+            raise BitnetError(BITNET_ERR_UNSUPPORTED_SHAPE, "bitnet_route")
+        out = tuple(_empty(torch, logits, s, torch.float32 if i == 1 else torch.int32, stream) for i, s in enumerate(shapes))
+    if len(out) != 5:
+        raise ValueError("out must be (chosen, gates, starts, rows, slots)")
+    ptrs = [_on_device(t, n, dev, torch.float32 if n == "gates" else torch.int32, s)
+            for t, n, s in zip(out, ("chosen", "gates", "starts", "rows", "slots"), shapes)]
+    wp, nb = None, 0
+    if workspace is None and need:
+        workspace = _empty(torch, logits, (need,), torch.uint8, stream)
+    if workspace is not None:
+        wp, nb = _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel()
+        if nb < need:
+            raise ValueError(f"workspace must hold at least {need} bytes")
+    _ok(lib().bitnet_route(logits.data_ptr(), dt, logits.stride(0) if T > 1 else E, T, E, k, bool(over_all), *ptrs, wp, nb,
+                           _launch_stream(torch, stream, dev)), "bitnet_route")
+    return tuple(out)
+
+
+def bitnet_w2a8_grouped(packed, scales, q, s_a, starts, N: int, K: int, rows=None, bias=None, act="none", gated: bool = False,
+                        out_dtype=None, y=None, stream=None):
+    """bitnet_w2a8_linear by expert: packed and scales hold the experts' matrices one behind the other, starts int32 [E + 1] says
+    which rows of y are whose, rows int32 [slots] which token each is of (without it row i is token i); bias fp32 [E][N].
+    Returns y [slots][N, or N/2 when gated] in out_dtype (bf16 by default); rows of no expert are not written."""
+    torch = _torch or _import_torch()
+    code = _act_code(act)
+    if starts.dim() != 1 or starts.shape[0] < 2:
+        raise ValueError("starts must be [experts + 1]")
+    E = starts.shape[0] - 1
+    dev, pp, sp, qp, sap, tokens = _product_ptrs(torch, packed, scales, q, s_a, N, K, E)
+    stp = _on_device(starts, "starts", dev, torch.int32)
+    rp, slots = None, tokens
+    if rows is not None:
+        rp = _on_device(rows, "rows", dev, torch.int32)
+        slots = rows.numel()
+        _bound(slots, "slots")
+    shape = (slots, N // 2 if gated else N)
+    bp = None if bias is None else _on_device(bias, "bias", dev, torch.float32, (E, N))
+    if y is None:
+        y = _empty(torch, q, shape, out_dtype or torch.bfloat16, stream)
+    yp, ydt = _on_device(y, "y", dev, out_dtype, shape), _float_dt(torch, y, "y")
+    _ok(lib().bitnet_w2a8_grouped(pp, sp, qp, sap, tokens, stp, rp, E, slots, bp, code, bool(gated), yp, ydt, N, K,
+                                  _launch_stream(torch, stream, dev)), "bitnet_w2a8_grouped")
+    return y
+
+
 # ------------------------------------------------------------------ convenience
 @dataclass
 class KVCache:
@@ -837,6 +1045,35 @@ class PackedWeight:
     def gemm(self, q, s_a, out_dtype=None, y=None, stream=None):
         return bitnet_w2a8_gemm(self.packed, self.scales, q, s_a, self.N, self.K, out_dtype=out_dtype, y=y,
                                 stream=stream)
+
+    def linear(self, q, s_a, **kw):
+        return bitnet_w2a8_linear(self.packed, self.scales, q, s_a, self.N, self.K, **kw)
+
+
+@dataclass
+class PackedExperts:
+    """Ternary weight matrices of one shape, an expert each, one behind the other in device memory in the tile layout."""
+    packed: object   # torch uint8 [experts * N*K/4] on device
+    scales: object   # torch fp32 [experts * N*K/128] on device (tiled order)
+    experts: int
+    N: int
+    K: int
+
+    @classmethod
+    def from_ternary(cls, ternary: np.ndarray, scales: np.ndarray, device="cuda"):
+        """ternary int8 [experts][N][K], scales fp32 [experts][N][K/128]."""
+        import torch
+        E, N, K = ternary.shape
+        # rows of 16 and their scales lie one behind the other, so the experts are packed as one tall matrix
+        p, s = bitnet_pack_i2s(ternary.reshape(E * N, K), scales.reshape(E * N, -1))
+        if bitnet_packed_bytes(N, K) == 0:
+            raise BitnetError(BITNET_ERR_UNSUPPORTED_SHAPE, "PackedExperts")
+        return cls(torch.from_numpy(p).to(device), torch.from_numpy(s).to(device), E, N, K)
+
+    def grouped(self, q, s_a, starts, **kw):
+        if starts.shape[0] != self.experts + 1:
+            raise ValueError(f"starts must be [{self.experts + 1}]")
+        return bitnet_w2a8_grouped(self.packed, self.scales, q, s_a, starts, self.N, self.K, **kw)
 
 
 # ------------------------------------------------------------------ chained decode

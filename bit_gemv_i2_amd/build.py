@@ -6,6 +6,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -14,7 +15,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libbitnet_w2a8.so")
 SOURCES = [os.path.join(CSRC, "bitnet_w2a8.hip"), os.path.join(CSRC, "pack.cpp"), os.path.join(CSRC, "probe.hip"),
            os.path.join(CSRC, "gemv_lut.hip"), os.path.join(CSRC, "rope.cpp"), os.path.join(CSRC, "kv_append.hip"),
-           os.path.join(CSRC, "attn_decode.hip"), os.path.join(CSRC, "attn_prompt.hip")]
+           os.path.join(CSRC, "attn_decode.hip"), os.path.join(CSRC, "attn_prompt.hip"),
+           os.path.join(CSRC, "norm_quant.hip"), os.path.join(CSRC, "route.hip"), os.path.join(CSRC, "w2a8_fused.hip")]
 HEADERS = [os.path.join(INCLUDE, "bitnet_w2a8.h"), os.path.join(CSRC, "layout.h"), os.path.join(CSRC, "attention.h")]
 ARCH = "gfx950"
 
@@ -35,19 +37,22 @@ def stale() -> bool:
 
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
-    objs = []
     common = ["-O3", "-std=c++17", "-fPIC", "-I" + INCLUDE, "-I" + CSRC, "-Wall"]
     # Packed fp32 VALU instructions stay off in device code.
     dev = ["-x", "hip", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
     build_dir = os.path.join(HERE, "_build")
     os.makedirs(build_dir, exist_ok=True)
-    for src in SOURCES:
+
+    def compile_one(src):
         obj = os.path.join(build_dir, os.path.basename(src) + ".o")
         cmd = [hipcc()] + common + (dev if src.endswith(".hip") else []) + ["-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         subprocess.check_call(cmd)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(4) as pool:  # a compiler each
+        objs = list(pool.map(compile_one, SOURCES))
     cmd = [hipcc(), "-shared", f"--offload-arch={ARCH}", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), file=sys.stderr)

@@ -542,6 +542,98 @@ bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, const void *
                                    int q_heads, int kv_heads, int head_dim, int causal, float scale, void *out,
                                    hipStream_t stream);
 
+/* ---------------------------------------------------------------- between the products of a decoder layer
+ *
+ * What stands before and behind a product: the residual stream with its norm and quantiser,
+ * and products whose epilogue adds a bias, activates and adds the residual. */
+
+/* Residual addition, root-mean-square norm and quantisation in one pass over the stream:
+ *     v = x + d,   d = add[m], or with slots  d = sum_j gates[m][j] * add[slots[m][j]]
+ *     x_out[m] = v rounded to x's type (the norm is of these values, so that a later norm of x_out is the same)
+ *     r[m] = 1 / sqrt(mean_k x_out^2 + eps)   (in 64 bits, rounded once to fp32)
+ *     h = (x_out * r) * weight
+ *     q, s_a: h quantised exactly as bitnet_quant_act does;  h_out: h rounded to hdt.
+ * Every product and sum is rounded by itself in fp32; d begins at 0 and takes its parts in the order of j.
+ *   x        device, [M][K], xdt BITNET_DT_BF16 or BITNET_DT_F32
+ *   add      device, adt BITNET_DT_BF16 or BITNET_DT_F32: [M][K], or with slots [add_rows][K]; NULL: v = x
+ *   slots    device, int32 [M][parts], or NULL (parts 0): rows of add, as bitnet_route gives them; a part whose
+ *            slot lies outside 0 .. add_rows - 1 is left out, its gate unread
+ *   gates    device, fp32 [M][parts], with slots only
+ *   weight   device, fp32 [K], or NULL for ones
+ *   x_out    device, [M][K] of xdt (out); may be x itself, must not overlap add; NULL without add
+ *   q, s_a   device, int8 [M][K] and fp32 [M] (out), or both NULL
+ *   h_out    device, [M][K], hdt BITNET_DT_BF16 or BITNET_DT_F32 (out), or NULL
+ * A row whose h holds an infinity or a NaN (of x, add, a gate or the weight) has s_a = NaN and codes of 0, so that
+ * every product of it is NaN; other rows do not see it.
+ * Rules: M >= 1; 16 <= K <= 65536, K % 16 == 0; with slots 1 <= parts <= 64 and add_rows >= 1; eps > 0 and finite; one of q and
+ * h_out at least. */
+bitnet_status_t bitnet_add_norm(const void *x, int xdt, const void *add, int adt, int64_t add_rows,
+                                const int32_t *slots, const float *gates, int parts, const float *weight, float eps,
+                                int M, int K, void *x_out, int8_t *q, float *s_a, void *h_out, int hdt,
+                                hipStream_t stream);
+
+/* Activations of the products below, in fp32. */
+typedef enum {
+    BITNET_ACT_NONE = 0,
+    BITNET_ACT_RELU = 1,  /* max(z, 0) */
+    BITNET_ACT_RELU2 = 2, /* max(z, 0)^2 */
+    BITNET_ACT_SILU = 3,  /* z / (1 + exp(-z)) */
+    BITNET_ACT_GELU = 4   /* z / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3), which is z (1 + tanh u) / 2 */
+} bitnet_act_t;
+
+/* W2A8 product with an epilogue, any number of tokens:
+ *     z[m][n] = s_a[m] * sum_b S[n][b] * A[m][n][b] + bias[n]
+ *     y[m][n] = act(z[m][n]) + residual[m][n]                          n < N
+ * or, gated (the gate in rows 0 .. N/2 - 1 of the weights, the up projection in the others, as the relu2_glu junction has them):
+ *     y[m][n] = act(z[m][n]) * z[m][N/2 + n] + residual[m][n]           n < N/2
+ * in fp32 (z as bitnet_w2a8_gemv has it, within 1e-5 of max(|.|, s_a * sum_b |S*A|) before the bias), rounded once to ydt.
+ *   packed, scales, q, s_a   as bitnet_w2a8_gemm
+ *   bias      device, fp32 [N], or NULL
+ *   residual  device, [M][width of y], rdt BITNET_DT_BF16 or BITNET_DT_F32, or NULL; may be y itself when of the same type
+ *   y         device, ydt BITNET_DT_BF16 or BITNET_DT_F32 (out)
+ * A token whose s_a is NaN has rows of NaN (the activations keep a NaN); other tokens do not see it.
+ * Rules: the shape rules, M >= 1, N % 32 == 0 when gated. */
+bitnet_status_t bitnet_w2a8_linear(const uint8_t *packed, const float *scales, const int8_t *q, const float *s_a,
+                                   const float *bias, int act, int gated, const void *residual, int rdt, void *y,
+                                   int ydt, int M, int N, int K, hipStream_t stream);
+
+/* ---------------------------------------------------------------- a layer of experts
+ *
+ * Tokens are sorted by expert without the host's knowing how many each has: bitnet_route chooses and sorts,
+ * bitnet_w2a8_grouped multiplies each expert's rows by its weights, bitnet_add_norm (slots) brings the results home. */
+
+/* The experts of each token and the sorted plan.  Of every token the k experts of the largest logits, the lower index first
+ * among equals; an expert whose logit is minus infinity or NaN is never chosen, and places that stay empty hold expert -1, gate 0,
+ * slot -1 (a token of padding: all logits minus infinity).  Gates are the softmax of the chosen logits, or with `over_all` their
+ * share of the softmax over all experts.  An infinite logit gives gates of NaN.
+ * Slots: assignments sorted by expert, by token within an expert.
+ *   logits   device, [tokens][experts], dt BITNET_DT_BF16 or BITNET_DT_F32, rows row_stride elements apart
+ *   chosen   device, int32 [tokens][k] (out): experts in the order of their logits
+ *   gates    device, fp32 [tokens][k] (out)
+ *   starts   device, int32 [experts + 1] (out): slots starts[e] .. starts[e+1] - 1 are expert e's
+ *   rows     device, int32 [tokens * k] (out): the token of every slot, -1 behind the last one
+ *   slots    device, int32 [tokens][k] (out): the slot of every assignment, or -1
+ *   workspace  device, 16-byte aligned, >= bitnet_route_workspace_bytes(...); clobbered; may be NULL where that is 0
+ * Rules: 1 <= k <= 32, k <= experts <= 1024, tokens >= 1, tokens * k <= 2^30; row_stride >= experts.  Outputs do not overlap. */
+size_t bitnet_route_workspace_bytes(int tokens, int experts, int k);
+bitnet_status_t bitnet_route(const void *logits, int dt, int64_t row_stride, int tokens, int experts, int k,
+                             int over_all, int32_t *chosen, float *gates, int32_t *starts, int32_t *rows,
+                             int32_t *slots, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* bitnet_w2a8_linear by expert, without a residual: row i of y, starts[e] <= i < starts[e+1], is the product of token rows[i] (or
+ * of row i of q, without rows) with the weights of expert e.
+ *   packed, scales  device, the experts' matrices one behind the other (bitnet_packed_bytes and bitnet_scale_count each)
+ *   q, s_a    device, int8 [tokens][K] and fp32 [tokens]
+ *   starts    device, int32 [experts + 1], not falling; read as lying within 0 .. slots
+ *   rows      device, int32 [slots], or NULL; a row outside 0 .. tokens - 1 is not followed and its row of y not written
+ *   bias      device, fp32 [experts][N], or NULL
+ *   y         device, [slots][N, or N/2 when gated] of ydt (out); rows of no expert are not written
+ * Rules: as bitnet_w2a8_linear; 1 <= experts <= 1024; 1 <= slots, tokens <= 2^30; without rows tokens >= slots. */
+bitnet_status_t bitnet_w2a8_grouped(const uint8_t *packed, const float *scales, const int8_t *q, const float *s_a,
+                                    int tokens, const int32_t *starts, const int32_t *rows, int experts, int slots,
+                                    const float *bias, int act, int gated, void *y, int ydt, int N, int K,
+                                    hipStream_t stream);
+
 /* ---------------------------------------------------------------- measurement helper */
 
 /* Not part of the product path: one pass of 16-byte non-temporal (streaming)
