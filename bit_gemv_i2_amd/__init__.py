@@ -117,10 +117,12 @@ _SIGS = {
                          ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_int]
                         + [ctypes.c_void_p] * 4 + [ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
     "bitnet_w2a8_linear": ([ctypes.c_void_p] * 5 + [ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]
-                           + [ctypes.c_int] * 4 + [ctypes.c_void_p], ctypes.c_int),
+                           + [ctypes.c_int] * 4 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "bitnet_w2a8_linear_workspace_bytes": ([ctypes.c_int] * 3, ctypes.c_size_t),
+    "bitnet_w2a8_grouped_workspace_bytes": ([ctypes.c_int] * 5, ctypes.c_size_t),
     "bitnet_w2a8_grouped": ([ctypes.c_void_p] * 4 + [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
                              ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p] + [ctypes.c_int] * 3
-                            + [ctypes.c_void_p], ctypes.c_int),
+                            + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
     "bitnet_route_workspace_bytes": ([ctypes.c_int] * 3, ctypes.c_size_t),
     "bitnet_route": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int64] + [ctypes.c_int] * 4 + [ctypes.c_void_p] * 6
                      + [ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
@@ -893,6 +895,17 @@ def _product_ptrs(torch, packed, scales, q, s_a, N, K, matrices):
     return dev, pp, sp, _on_device(q, "q", dev, torch.int8), _on_device(s_a, "s_a", dev, torch.float32, (M,)), M
 
 
+def _workspace(torch, given, need: int, like, dev: int, stream):
+    """(pointer, bytes) of the workspace given, or of one made where any is needed."""
+    if given is None:
+        if not need:
+            return None, 0
+        given = _empty(torch, like, (need,), torch.uint8, stream)
+    elif given.numel() < need:
+        raise ValueError(f"workspace must hold at least {need} bytes")
+    return _on_device(given, "workspace", dev, torch.uint8), given.numel()
+
+
 def _i64(n: int) -> int:
     if not -1 << 63 <= n < 1 << 63:
         raise ValueError("a size must be below 2^63")
@@ -900,7 +913,7 @@ def _i64(n: int) -> int:
 
 
 def bitnet_w2a8_linear(packed, scales, q, s_a, N: int, K: int, bias=None, act="none", gated: bool = False, residual=None,
-                       out_dtype=None, y=None, stream=None):
+                       out_dtype=None, y=None, workspace=None, stream=None):
     """W2A8 product with an epilogue, any number of tokens: act(z) + residual, or gated act(z[:, :N/2]) * z[:, N/2:] + residual, with
     z = product + bias.  act: "none", "relu", "relu2", "silu" or "gelu"; bias fp32 [N]; residual bf16 or fp32 of y's shape (y itself
     serves).  Returns y [M][N, or N/2 when gated] in out_dtype (y's, else the residual's, else bf16)."""
@@ -917,7 +930,8 @@ def bitnet_w2a8_linear(packed, scales, q, s_a, N: int, K: int, bias=None, act="n
     if y is None:
         y = _empty(torch, q, shape, out_dtype or (torch.bfloat16 if residual is None else residual.dtype), stream)
     yp, ydt = _on_device(y, "y", dev, out_dtype, shape), _float_dt(torch, y, "y")
-    _ok(lib().bitnet_w2a8_linear(pp, sp, qp, sap, bp, code, bool(gated), rp, rdt, yp, ydt, M, N, K,
+    wp, nb = _workspace(torch, workspace, lib().bitnet_w2a8_linear_workspace_bytes(M, N, K), q, dev, stream)
+    _ok(lib().bitnet_w2a8_linear(pp, sp, qp, sap, bp, code, bool(gated), rp, rdt, yp, ydt, M, N, K, wp, nb,
                                  _launch_stream(torch, stream, dev)), "bitnet_w2a8_linear")
     return y
 
@@ -954,20 +968,14 @@ def bitnet_route(logits, k: int, over_all: bool = False, out=None, workspace=Non
         raise ValueError("out must be (chosen, gates, starts, rows, slots)")
     ptrs = [_on_device(t, n, dev, torch.float32 if n == "gates" else torch.int32, s)
             for t, n, s in zip(out, ("chosen", "gates", "starts", "rows", "slots"), shapes)]
-    wp, nb = None, 0
-    if workspace is None and need:
-        workspace = _empty(torch, logits, (need,), torch.uint8, stream)
-    if workspace is not None:
-        wp, nb = _on_device(workspace, "workspace", dev, torch.uint8), workspace.numel()
-        if nb < need:
-            raise ValueError(f"workspace must hold at least {need} bytes")
+    wp, nb = _workspace(torch, workspace, need, logits, dev, stream)
     _ok(lib().bitnet_route(logits.data_ptr(), dt, logits.stride(0) if T > 1 else E, T, E, k, bool(over_all), *ptrs, wp, nb,
                            _launch_stream(torch, stream, dev)), "bitnet_route")
     return tuple(out)
 
 
 def bitnet_w2a8_grouped(packed, scales, q, s_a, starts, N: int, K: int, rows=None, bias=None, act="none", gated: bool = False,
-                        out_dtype=None, y=None, stream=None):
+                        out_dtype=None, y=None, workspace=None, stream=None):
     """bitnet_w2a8_linear by expert: packed and scales hold the experts' matrices one behind the other, starts int32 [E + 1] says
     which rows of y are whose, rows int32 [slots] which token each is of (without it row i is token i); bias fp32 [E][N].
     Returns y [slots][N, or N/2 when gated] in out_dtype (bf16 by default); rows of no expert are not written."""
@@ -988,7 +996,8 @@ def bitnet_w2a8_grouped(packed, scales, q, s_a, starts, N: int, K: int, rows=Non
     if y is None:
         y = _empty(torch, q, shape, out_dtype or torch.bfloat16, stream)
     yp, ydt = _on_device(y, "y", dev, out_dtype, shape), _float_dt(torch, y, "y")
-    _ok(lib().bitnet_w2a8_grouped(pp, sp, qp, sap, tokens, stp, rp, E, slots, bp, code, bool(gated), yp, ydt, N, K,
+    wp, nb = _workspace(torch, workspace, lib().bitnet_w2a8_grouped_workspace_bytes(tokens, slots, E, N, K), q, dev, stream)
+    _ok(lib().bitnet_w2a8_grouped(pp, sp, qp, sap, tokens, stp, rp, E, slots, bp, code, bool(gated), yp, ydt, N, K, wp, nb,
                                   _launch_stream(torch, stream, dev)), "bitnet_w2a8_grouped")
     return y
 

@@ -16,8 +16,10 @@ LIB = os.path.join(HERE, "libbitnet_w2a8.so")
 SOURCES = [os.path.join(CSRC, "bitnet_w2a8.hip"), os.path.join(CSRC, "pack.cpp"), os.path.join(CSRC, "probe.hip"),
            os.path.join(CSRC, "gemv_lut.hip"), os.path.join(CSRC, "rope.cpp"), os.path.join(CSRC, "kv_append.hip"),
            os.path.join(CSRC, "attn_decode.hip"), os.path.join(CSRC, "attn_prompt.hip"),
-           os.path.join(CSRC, "norm_quant.hip"), os.path.join(CSRC, "route.hip"), os.path.join(CSRC, "w2a8_fused.hip")]
-HEADERS = [os.path.join(INCLUDE, "bitnet_w2a8.h"), os.path.join(CSRC, "layout.h"), os.path.join(CSRC, "attention.h")]
+           os.path.join(CSRC, "norm_quant.hip"), os.path.join(CSRC, "route.hip"), os.path.join(CSRC, "w2a8_fused.hip"),
+           os.path.join(CSRC, "w2a8_tiles.hip")]
+HEADERS = [os.path.join(INCLUDE, "bitnet_w2a8.h"), os.path.join(CSRC, "layout.h"), os.path.join(CSRC, "attention.h"),
+           os.path.join(CSRC, "fused.h")]
 ARCH = "gfx950"
 
 

@@ -592,10 +592,13 @@ typedef enum {
  *   residual  device, [M][width of y], rdt BITNET_DT_BF16 or BITNET_DT_F32, or NULL; may be y itself when of the same type
  *   y         device, ydt BITNET_DT_BF16 or BITNET_DT_F32 (out)
  * A token whose s_a is NaN has rows of NaN (the activations keep a NaN); other tokens do not see it.
- * Rules: the shape rules, M >= 1, N % 32 == 0 when gated. */
+ *   workspace  device, 16-byte aligned, >= bitnet_w2a8_linear_workspace_bytes(M, N, K); clobbered; may be NULL where that is 0
+ * Rules: the shape rules, 1 <= M <= 2^24, N % 32 == 0 when gated. */
+size_t bitnet_w2a8_linear_workspace_bytes(int M, int N, int K);
 bitnet_status_t bitnet_w2a8_linear(const uint8_t *packed, const float *scales, const int8_t *q, const float *s_a,
                                    const float *bias, int act, int gated, const void *residual, int rdt, void *y,
-                                   int ydt, int M, int N, int K, hipStream_t stream);
+                                   int ydt, int M, int N, int K, void *workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
 
 /* ---------------------------------------------------------------- a layer of experts
  *
@@ -628,11 +631,13 @@ bitnet_status_t bitnet_route(const void *logits, int dt, int64_t row_stride, int
  *   rows      device, int32 [slots], or NULL; a row outside 0 .. tokens - 1 is not followed and its row of y not written
  *   bias      device, fp32 [experts][N], or NULL
  *   y         device, [slots][N, or N/2 when gated] of ydt (out); rows of no expert are not written
- * Rules: as bitnet_w2a8_linear; 1 <= experts <= 1024; 1 <= slots, tokens <= 2^30; without rows tokens >= slots. */
+ *   workspace  device, 16-byte aligned, >= bitnet_w2a8_grouped_workspace_bytes(...); clobbered; may be NULL where that is 0
+ * Rules: as bitnet_w2a8_linear; 1 <= experts <= 1024; 1 <= slots, tokens <= 2^24; without rows tokens >= slots. */
+size_t bitnet_w2a8_grouped_workspace_bytes(int tokens, int slots, int experts, int N, int K);
 bitnet_status_t bitnet_w2a8_grouped(const uint8_t *packed, const float *scales, const int8_t *q, const float *s_a,
                                     int tokens, const int32_t *starts, const int32_t *rows, int experts, int slots,
                                     const float *bias, int act, int gated, void *y, int ydt, int N, int K,
-                                    hipStream_t stream);
+                                    void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------- measurement helper */
 

@@ -38,8 +38,8 @@ def test_add_norm_refusals():
 
 
 def test_linear_refusals():
-    order = "packed scales q s_a bias act gated residual rdt y ydt M N K stream".split()
-    base = dict(packed=P, scales=P, q=P, s_a=P, bias=P, act=0, gated=0, residual=P, rdt=F32, y=P2, ydt=BF16, M=5, N=48, K=256, stream=NULL)
+    order = "packed scales q s_a bias act gated residual rdt y ydt M N K ws bytes stream".split()
+    base = dict(ws=NULL, bytes=0, packed=P, scales=P, q=P, s_a=P, bias=P, act=0, gated=0, residual=P, rdt=F32, y=P2, ydt=BF16, M=5, N=48, K=256, stream=NULL)
     f = bn.lib().bitnet_w2a8_linear
     for n in ("packed", "scales", "q", "y"):
         for v in (NULL, MIS):
@@ -47,13 +47,13 @@ def test_linear_refusals():
     for kw in (dict(s_a=NULL), dict(s_a=MIS4), dict(bias=MIS), dict(residual=MIS), dict(act=-1), dict(act=5), dict(rdt=2), dict(ydt=-1),
                dict(ydt=2), dict(residual=P2)):
         assert _call(f, order, base, **kw) == ARG, kw
-    for kw in (dict(M=0), dict(M=-4), dict(N=0), dict(N=40), dict(N=-16), dict(K=64), dict(K=0), dict(gated=1), dict(N=1 << 30, K=1 << 20)):
+    for kw in (dict(M=0), dict(M=-4), dict(M=(1 << 24) + 1), dict(N=0), dict(N=40), dict(N=-16), dict(K=64), dict(K=0), dict(gated=1), dict(N=1 << 30, K=1 << 20)):
         assert _call(f, order, base, **kw) == SHAPE, kw
 
 
 def test_grouped_refusals():
-    order = "packed scales q s_a tokens starts rows experts slots bias act gated y ydt N K stream".split()
-    base = dict(packed=P, scales=P, q=P, s_a=P, tokens=7, starts=P, rows=P, experts=4, slots=9, bias=P, act=0, gated=0, y=P, ydt=BF16, N=48,
+    order = "packed scales q s_a tokens starts rows experts slots bias act gated y ydt N K ws bytes stream".split()
+    base = dict(ws=NULL, bytes=0, packed=P, scales=P, q=P, s_a=P, tokens=7, starts=P, rows=P, experts=4, slots=9, bias=P, act=0, gated=0, y=P, ydt=BF16, N=48,
                 K=256, stream=NULL)
     f = bn.lib().bitnet_w2a8_grouped
     for n in ("packed", "scales", "q", "y"):
@@ -61,9 +61,28 @@ def test_grouped_refusals():
             assert _call(f, order, base, **{n: v}) == ARG, n
     for kw in (dict(s_a=NULL), dict(starts=NULL), dict(starts=MIS4), dict(rows=MIS4), dict(bias=MIS), dict(act=9), dict(ydt=3)):
         assert _call(f, order, base, **kw) == ARG, kw
-    for kw in (dict(tokens=0), dict(tokens=(1 << 30) + 1), dict(slots=0), dict(slots=-1), dict(slots=(1 << 30) + 1), dict(experts=0),
+    for kw in (dict(tokens=0), dict(tokens=(1 << 24) + 1), dict(slots=0), dict(slots=-1), dict(slots=(1 << 24) + 1), dict(experts=0),
                dict(experts=1025), dict(rows=NULL), dict(gated=1), dict(N=24), dict(K=100)):
         assert _call(f, order, base, **kw) == SHAPE, kw
+
+
+def test_product_workspaces():
+    """Few rows an expert need none; many need the digits of every token, which a call without them is refused."""
+    assert bn.lib().bitnet_w2a8_linear_workspace_bytes(1, 32, 256) == 0
+    assert bn.lib().bitnet_w2a8_linear_workspace_bytes(4000, 32, 256) == 4000 * 2 * 192
+    assert bn.lib().bitnet_w2a8_linear_workspace_bytes(1 << 24, 32, 256) == (1 << 24) * 2 * 192
+    assert bn.lib().bitnet_w2a8_grouped_workspace_bytes(4000, 8000, 8, 32, 256) == 4000 * 2 * 192
+    assert bn.lib().bitnet_w2a8_grouped_workspace_bytes(40, 80, 80, 32, 256) == 0
+    for bad in ((0, 32, 256), (4000, 40, 256), (4000, 32, 100)):
+        assert bn.lib().bitnet_w2a8_linear_workspace_bytes(*bad) == 0
+    for bad in ((0, 80, 2, 32, 256), (40, 0, 2, 32, 256), (40, 80, 0, 32, 256), (40, 80, 2, 33, 256), (-1, 80, 2, 32, 256)):
+        assert bn.lib().bitnet_w2a8_grouped_workspace_bytes(*bad) == 0
+    f = bn.lib().bitnet_w2a8_linear
+    need = bn.lib().bitnet_w2a8_linear_workspace_bytes(4000, 32, 256)
+    for ws, nb in ((NULL, 0), (NULL, need), (P, need - 1), (MIS, need)):
+        assert f(P, P, P, P, NULL, 0, 0, NULL, 0, P2, F32, 4000, 32, 256, ws, nb, NULL) == ARG
+    for ws, nb in ((NULL, 0), (P, need - 1), (MIS, need)):
+        assert bn.lib().bitnet_w2a8_grouped(P, P, P, P, 4000, P, P, 2, 4000, NULL, 0, 0, P2, F32, 32, 256, ws, nb, NULL) == ARG
 
 
 def test_route_refusals():
