@@ -828,7 +828,9 @@ def _add_norm(name, x, weight, eps, add, slots, gates, x_out, q, s_a, h, h_dtype
             gp = _on_device(gates, "gates", dev, torch.float32, slots.shape)
         if x_out is None:
             x_out = _empty(torch, x, (M, K), x.dtype, stream)
-        op = _on_device(x_out, "x_out", dev, x.dtype, x.shape)
+            op = x_out.data_ptr()
+        else:
+            op = _on_device(x_out, "x_out", dev, x.dtype, x.shape)
     else:
         if x_out is not None:
             raise ValueError("x_out comes with add")
@@ -839,9 +841,14 @@ def _add_norm(name, x, weight, eps, add, slots, gates, x_out, q, s_a, h, h_dtype
     if h_dtype is None:
         if q is None:
             q = _empty(torch, x, (M, K), torch.int8, stream)
+            qp = q.data_ptr()
+        else:
+            qp = _on_device(q, "q", dev, torch.int8, x.shape)
         if s_a is None:
             s_a = _empty(torch, x, (M,), torch.float32, stream)
-        qp, sap = _on_device(q, "q", dev, torch.int8, x.shape), _on_device(s_a, "s_a", dev, torch.float32, (M,))
+            sap = s_a.data_ptr()
+        else:
+            sap = _on_device(s_a, "s_a", dev, torch.float32, (M,))
     else:
         if h is None:
             h = _empty(torch, x, (M, K), h_dtype, stream)
@@ -929,7 +936,10 @@ def bitnet_w2a8_linear(packed, scales, q, s_a, N: int, K: int, bias=None, act="n
             raise ValueError(f"residual must be {list(shape)}, not {tuple(residual.shape)}")
     if y is None:
         y = _empty(torch, q, shape, out_dtype or (torch.bfloat16 if residual is None else residual.dtype), stream)
-    yp, ydt = _on_device(y, "y", dev, out_dtype, shape), _float_dt(torch, y, "y")
+        yp = y.data_ptr()
+    else:
+        yp = _on_device(y, "y", dev, out_dtype, shape)
+    ydt = _float_dt(torch, y, "y")
     wp, nb = _workspace(torch, workspace, lib().bitnet_w2a8_linear_workspace_bytes(M, N, K), q, dev, stream)
     _ok(lib().bitnet_w2a8_linear(pp, sp, qp, sap, bp, code, bool(gated), rp, rdt, yp, ydt, M, N, K, wp, nb,
                                  _launch_stream(torch, stream, dev)), "bitnet_w2a8_linear")
@@ -958,16 +968,21 @@ def bitnet_route(logits, k: int, over_all: bool = False, out=None, workspace=Non
     dev = logits.get_device()
     if dev < 0:
         raise ValueError("logits must be a device tensor")
-    need = bitnet_route_workspace_bytes(T, E, k)
-    shapes = ((T, k), (T, k), (E + 1,), (T * k,), (T, k))
+    need = lib().bitnet_route_workspace_bytes(T, E, k)
     if out is None:
         if T < 1 or not 1 <= k <= E:
             raise BitnetError(BITNET_ERR_UNSUPPORTED_SHAPE, "bitnet_route")
-        out = tuple(_empty(torch, logits, s, torch.float32 if i == 1 else torch.int32, stream) for i, s in enumerate(shapes))
-    if len(out) != 5:
-        raise ValueError("out must be (chosen, gates, starts, rows, slots)")
-    ptrs = [_on_device(t, n, dev, torch.float32 if n == "gates" else torch.int32, s)
-            for t, n, s in zip(out, ("chosen", "gates", "starts", "rows", "slots"), shapes)]
+        i32 = torch.int32
+        out = (_empty(torch, logits, (T, k), i32, stream), _empty(torch, logits, (T, k), torch.float32, stream),
+               _empty(torch, logits, (E + 1,), i32, stream), _empty(torch, logits, (T * k,), i32, stream),
+               _empty(torch, logits, (T, k), i32, stream))
+        ptrs = [t.data_ptr() for t in out]
+    else:
+        if len(out) != 5:
+            raise ValueError("out must be (chosen, gates, starts, rows, slots)")
+        shapes = ((T, k), (T, k), (E + 1,), (T * k,), (T, k))
+        ptrs = [_on_device(t, n, dev, torch.float32 if n == "gates" else torch.int32, s)
+                for t, n, s in zip(out, ("chosen", "gates", "starts", "rows", "slots"), shapes)]
     wp, nb = _workspace(torch, workspace, need, logits, dev, stream)
     _ok(lib().bitnet_route(logits.data_ptr(), dt, logits.stride(0) if T > 1 else E, T, E, k, bool(over_all), *ptrs, wp, nb,
                            _launch_stream(torch, stream, dev)), "bitnet_route")
@@ -995,7 +1010,10 @@ def bitnet_w2a8_grouped(packed, scales, q, s_a, starts, N: int, K: int, rows=Non
     bp = None if bias is None else _on_device(bias, "bias", dev, torch.float32, (E, N))
     if y is None:
         y = _empty(torch, q, shape, out_dtype or torch.bfloat16, stream)
-    yp, ydt = _on_device(y, "y", dev, out_dtype, shape), _float_dt(torch, y, "y")
+        yp = y.data_ptr()
+    else:
+        yp = _on_device(y, "y", dev, out_dtype, shape)
+    ydt = _float_dt(torch, y, "y")
     wp, nb = _workspace(torch, workspace, lib().bitnet_w2a8_grouped_workspace_bytes(tokens, slots, E, N, K), q, dev, stream)
     _ok(lib().bitnet_w2a8_grouped(pp, sp, qp, sap, tokens, stp, rp, E, slots, bp, code, bool(gated), yp, ydt, N, K, wp, nb,
                                   _launch_stream(torch, stream, dev)), "bitnet_w2a8_grouped")
