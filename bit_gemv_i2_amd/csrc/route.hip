@@ -2,7 +2,9 @@
 //
 // A group of G lanes holds the logits of a token, a lane VPL neighbouring ones, as whole numbers in the order of the
 // floats (0: never chosen).  The k largest are taken one after the other: the largest of the group, the lowest lane that
-// holds it, which strikes it out.  Neighbours in a lane and the lowest lane make ties go to the lowest expert.
+// holds it, which strikes it out.  Neighbours in a lane and the lowest lane make ties go to the lowest expert.  The floor is one
+// read of the logits (6.3 MB of 16383 x 128 in bf16: 1 us); what bounds it is the issue of some 70 operations a round, which 8
+// tokens of a wave share, and the latency of a plan of three dependent steps.
 //
 // The plan is a counting sort.  64 tokens at a time: every expert has a 64-bit mask of the tokens that chose it, so
 // that an assignment's place among them is the count of the lower bits: the same plan whatever the order of the
@@ -22,13 +24,16 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kMaxExperts = 1024, kMaxChosen = 32;
 constexpr int kSub = 64;          // tokens of a mask
-constexpr int kOneLaunch = 256;   // tokens
+// Tokens up to which one workgroup does all (64 experts, 6 of them: 64 tokens 7.0 us, 128 10.4, 256 16.1; in two launches 65 to 512
+// tokens take 9.4 us, but a second call's time on the host).
+constexpr int kOneLaunch = 128;
+constexpr int kEach = 64;         // tokens of a workgroup, at least, of the two-launch form (16383 tokens, 8 of 128: 17.9 us; 128: 21.8)
 constexpr int kMostBlocks = 256;  // workgroups of the two-launch form
 
 struct RouteArgs {
     const void *logits;
     int64_t row_stride;
-    int tokens, experts, k, over_all, per_block;  // per_block: tokens of a workgroup, a multiple of kSub
+    int tokens, experts, k, over_all, per_block;  // per_block: tokens of a workgroup
     int32_t *chosen, *starts, *rows, *slots, *counts;
     float *gates;
 };
@@ -52,75 +57,111 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
+// Maximum and sum over G neighbouring lanes, the same in each: within 16 by DPP, then by swaps of rows and of halves.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+template <int G, typename F>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, F &&join) {
+    v = join(v, dpp<kXor1>(v));
+    v = join(v, dpp<kXor2>(v));
+    v = join(v, dpp<kHalfMirror>(v));
+    if constexpr (G > 8) v = join(v, dpp<kMirror>(v));
+    if constexpr (G > 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = join((uint32_t)r[0], (uint32_t)r[1]);
+    }
+    if constexpr (G > 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = join((uint32_t)r[0], (uint32_t)r[1]);
+    }
+    return v;
+}
 template <int G>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-#pragma unroll
-    for (int o = G / 2; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-    return v;
+    return group_reduce<G>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int o = G / 2; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    return __uint_as_float(group_reduce<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
 }
 
-// Experts and gates of tokens t0 .. t1 - 1 of this workgroup; every choice is counted in total[].
+// Experts and gates of tokens t0 .. t1 - 1 of this workgroup; every choice is counted in total[].  What a round costs is mostly what
+// its maximum over the group costs, so a group is as small as the registers allow (64 experts: 8 lanes of 8 and 8 tokens a wave
+// instead of 64 lanes and one).
+template <int G>
+struct Kept {  // the choices of every group's token
+    float value[kThreads / G][kMaxChosen + 1];
+    int16_t expert[kThreads / G][kMaxChosen + 2];
+};
+
 template <typename T, int G, int VPL>
-__device__ void choose(const RouteArgs &p, int t0, int t1, int *total) {
+__device__ void choose(const RouteArgs &p, int t0, int t1, int *total, Kept<G> &kept) {
     constexpr int kGroups = kThreads / G;
-    const int lane = threadIdx.x & 63, sub = lane & (G - 1), first = lane & ~(G - 1);
+    const int group = threadIdx.x / G, lane = threadIdx.x & 63, sub = lane & (G - 1), first = lane & ~(G - 1);
     const uint64_t mine = (G == 64 ? ~0ull : (1ull << (G & 63)) - 1) << first;
-    for (int t = t0 + (int)threadIdx.x / G; t - (int)threadIdx.x / G < t1; t += kGroups) {
-        const bool there = t < t1;
-        const T *row = static_cast<const T *>(p.logits) + (int64_t)(there ? t : t0) * p.row_stride;
-        uint32_t key[VPL];
+    for (int base = t0; base + (int)(threadIdx.x & ~63u) / G < t1; base += kGroups) {  // as long as the wave has a token
+        const int t = base + group;
+        const T *row = static_cast<const T *>(p.logits) + (int64_t)min(t, t1 - 1) * p.row_stride;
+        uint32_t left[VPL];
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             const int e = sub * VPL + v;
-            key[v] = e < p.experts ? key_of(as_float(row[e])) : 0;
+            const float x = as_float(row[min(e, p.experts - 1)]);
+            left[v] = e < p.experts ? key_of(x) : 0;
         }
-        uint32_t best = key[0];
+        uint32_t best = left[0];
 #pragma unroll
-        for (int v = 1; v < VPL; ++v) best = max(best, key[v]);
+        for (int v = 1; v < VPL; ++v) best = max(best, left[v]);
         uint32_t top = group_max<G>(best);
         const float most = value_of(top);
-        float all = 0.0f;
+        float sum = 0.0f;
         if (p.over_all) {
 #pragma unroll
-            for (int v = 0; v < VPL; ++v) all += key[v] ? expf(value_of(key[v]) - most) : 0.0f;
-            all = group_sum<G>(all);
+            for (int v = 0; v < VPL; ++v) sum += left[v] ? __expf(value_of(left[v]) - most) : 0.0f;
+            sum = group_sum<G>(sum);
         }
-        int expert = -1;
-        float gate = 0.0f;
+        // Lane j % G keeps choice j, in LDS.  A loop, not rounds in a row: the instructions of 32 rounds take longer to come than to run.
+        int16_t *expert = kept.expert[group];
+        float *value = kept.value[group];
+#pragma unroll 1
         for (int j = 0; j < p.k; ++j) {
-            if (j) top = group_max<G>(best);
-            const uint64_t who = __ballot(best == top && top) & mine;
-            const int winner = who ? __ffsll((unsigned long long)who) - 1 : 0;
-            int e = 0;
+            if (j) {
+                best = left[0];
 #pragma unroll
-            for (int v = VPL - 1; v >= 0; --v)
-                if (key[v] == best) e = v;
-            if (lane == winner && who) {
-#pragma unroll
-                for (int v = 0; v < VPL; ++v)
-                    if (v == e) key[v] = 0;
-                best = key[0];
-#pragma unroll
-                for (int v = 1; v < VPL; ++v) best = max(best, key[v]);
+                for (int v = 1; v < VPL; ++v) best = max(best, left[v]);
+                top = group_max<G>(best);
             }
-            e = __shfl(sub * VPL + e, winner);
-            if (sub == j) {
-                expert = who ? e : -1;
-                gate = who ? expf(value_of(top) - most) : 0.0f;
+            const uint64_t who = __ballot(best == top) & mine;  // the lowest lane and its first value that hold it
+            const int winner = __ffsll((unsigned long long)who) - 1;
+            int at = VPL - 1;
+#pragma unroll
+            for (int v = VPL - 2; v >= 0; --v) at = left[v] == top ? v : at;
+            const int struck = lane == winner ? at : -1;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) left[v] = v == struck ? 0 : left[v];
+            const int e = __shfl(sub * VPL + at, winner);
+            if (sub == (j & (G - 1))) {
+                expert[j] = (int16_t)(top ? e : -1);
+                value[j] = value_of(top);
             }
         }
-        const float sum = p.over_all ? all : group_sum<G>(sub < p.k ? gate : 0.0f);
-        if (there && sub < p.k) {
-            const int64_t at = (int64_t)t * p.k + sub;
-            p.chosen[at] = expert;
-            p.gates[at] = expert < 0 ? 0.0f : gate / sum;
-            if (expert >= 0) atomicAdd(&total[expert], 1);
+        if (!p.over_all) {
+            float part = 0.0f;
+#pragma unroll 1
+            for (int j = sub; j < p.k; j += G) part += expert[j] < 0 ? 0.0f : __expf(value[j] - most);
+            sum = group_sum<G>(part);
+        }
+        if (t >= t1) continue;
+#pragma unroll 1
+        for (int j = sub; j < p.k; j += G) {
+            const int e = expert[j];
+            const int64_t to = (int64_t)t * p.k + j;
+            p.chosen[to] = e;
+            p.gates[to] = e < 0 ? 0.0f : __expf(value[j] - most) / sum;
+            if (e >= 0) atomicAdd(&total[e], 1);
         }
     }
 }
@@ -189,11 +230,12 @@ __device__ void clear(const RouteArgs &p, Plan &s) {
 template <typename T, int G, int VPL>
 __global__ __launch_bounds__(kThreads) void choose_kernel(RouteArgs p) {
     __shared__ Plan s;
-    static_assert(kThreads == kMaxExperts, "a thread clears an expert");
+    __shared__ Kept<G> kept;
+    static_assert(kEach % kSub == 0 && kThreads == kMaxExperts, "a thread clears an expert");
     const int t0 = blockIdx.x * p.per_block, t1 = min(p.tokens, t0 + p.per_block);
     clear(p, s);
     __syncthreads();
-    choose<T, G, VPL>(p, t0, t1, s.total);
+    choose<T, G, VPL>(p, t0, t1, s.total, kept);
     __syncthreads();  // chosen[] of this workgroup is visible to it
     if (p.counts) {
         for (int e = threadIdx.x; e < p.experts; e += kThreads) p.counts[(int64_t)blockIdx.x * p.experts + e] = s.total[e];
@@ -216,10 +258,16 @@ __global__ __launch_bounds__(kThreads) void place_kernel(RouteArgs p) {
     const int e = threadIdx.x & (wide - 1);
     if (e < p.experts) {
         int all = 0, before = 0;
-        for (int b = threadIdx.x / wide; b < (int)gridDim.x; b += kThreads / wide) {
-            const int c = p.counts[(int64_t)b * p.experts + e];
-            all += c;
-            before += b < (int)blockIdx.x ? c : 0;
+        const int step = kThreads / wide;
+        for (int b = threadIdx.x / wide; b < (int)gridDim.x; b += 8 * step) {  // eight loads on their way at a time
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = p.counts[(int64_t)min(b + i * step, (int)gridDim.x - 1) * p.experts + e];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                all += b + i * step < (int)gridDim.x ? c[i] : 0;
+                before += b + i * step < (int)blockIdx.x ? c[i] : 0;
+            }
         }
         atomicAdd(&s.total[e], all);
         atomicAdd(&s.base[e], before);
@@ -238,22 +286,24 @@ int blocks_of(int tokens, int *per_block) {
         *per_block = kOneLaunch;
         return 1;
     }
-    const int subs = (tokens + kSub - 1) / kSub, each = (subs + kMostBlocks - 1) / kMostBlocks;
-    *per_block = each * kSub;
+    const int subs = (tokens + kEach - 1) / kEach, each = (subs + kMostBlocks - 1) / kMostBlocks;
+    *per_block = each * kEach;
     return (subs + each - 1) / each;
 }
 
 template <typename T>
 void launch_choose(const RouteArgs &p, int blocks, hipStream_t stream) {
     const dim3 grid(blocks), block(kThreads);
-    if (p.experts <= 8) hipLaunchKernelGGL((choose_kernel<T, 8, 1>), grid, block, 0, stream, p);
-    else if (p.experts <= 16) hipLaunchKernelGGL((choose_kernel<T, 16, 1>), grid, block, 0, stream, p);
-    else if (p.experts <= 32) hipLaunchKernelGGL((choose_kernel<T, 32, 1>), grid, block, 0, stream, p);
-    else if (p.experts <= 64) hipLaunchKernelGGL((choose_kernel<T, 64, 1>), grid, block, 0, stream, p);
-    else if (p.experts <= 128) hipLaunchKernelGGL((choose_kernel<T, 64, 2>), grid, block, 0, stream, p);
-    else if (p.experts <= 256) hipLaunchKernelGGL((choose_kernel<T, 64, 4>), grid, block, 0, stream, p);
-    else if (p.experts <= 512) hipLaunchKernelGGL((choose_kernel<T, 64, 8>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((choose_kernel<T, 64, 16>), grid, block, 0, stream, p);
+#define BITNET_CHOOSE(G, VPL) hipLaunchKernelGGL((choose_kernel<T, G, VPL>), grid, block, 0, stream, p)
+    if (p.experts <= 8) BITNET_CHOOSE(8, 1);
+    else if (p.experts <= 16) BITNET_CHOOSE(8, 2);
+    else if (p.experts <= 32) BITNET_CHOOSE(8, 4);
+    else if (p.experts <= 64) BITNET_CHOOSE(8, 8);
+    else if (p.experts <= 128) BITNET_CHOOSE(8, 16);
+    else if (p.experts <= 256) BITNET_CHOOSE(16, 16);
+    else if (p.experts <= 512) BITNET_CHOOSE(32, 16);
+    else BITNET_CHOOSE(64, 16);
+#undef BITNET_CHOOSE
 }
 
 bool sizes_ok(int tokens, int experts, int k) {
