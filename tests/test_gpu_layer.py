@@ -532,3 +532,14 @@ def test_results_repeat(gpu):
             again = b(x)
             for n in first:
                 assert torch.equal(first[n].view(torch.uint8), again[n].view(torch.uint8)), n
+
+
+def test_the_example_with_experts_runs(gpu):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import generate
+    model = generate.Decoder(2, 512, 4, 2, 256, experts=6, top=2)
+    tokens, states = model.generate([[3, 1, 4], [1] * 70, [5]], 4)
+    assert tokens.shape == (3, 4) and ((tokens >= 0) & (tokens < 4096)).all() and torch.isfinite(states).all()
+    assert -1 <= generate.check(model, [[3, 1, 4], [1] * 70, [5]], tokens, states) <= 1.0001
