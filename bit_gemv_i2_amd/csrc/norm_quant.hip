@@ -115,7 +115,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs p, int
     const int64_t m = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
     if (WAVE && m >= rows) return;
     const T *x = static_cast<const T *>(p.x) + m * p.K;
-    // chunks behind the row's end repeat its last one: they are not stored, and are left out of the sum (a maximum may see them twice)
+    // chunks behind the row's end repeat its last one; they count for nothing (where x_out is x, another wave may have stored that one)
     int at[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) at[c] = 8 * min(tid + c * threads, n - 1);
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs p, int
         for (int i = 0; i < 8; ++i) {
             f[c][i] *= r;
             if (p.weight) f[c][i] *= w[c][i];
-            most = max(most, magnitude(f[c][i]));
+            most = there(c) ? max(most, magnitude(f[c][i])) : most;
         }
         if (p.h_out && there(c)) {
             if (hdt == BITNET_DT_BF16) store8(static_cast<uint16_t *>(p.h_out) + m * p.K + at[c], f[c]);

@@ -445,6 +445,8 @@ bitnet_status_t run(const FusedArgs &p, int gated, void *workspace, size_t works
 }
 
 constexpr int kMostRows = 1 << 24;  // tokens and slots
+constexpr int kMostK = 1 << 24;     // offsets inside 16 rows of weights in 32 bits
+constexpr int64_t kMostWeights = (int64_t)1 << 34;  // of a matrix: scales' offsets in 32 bits, row tiles in a launch's size
 
 bool float_type(int dt) { return dt == BITNET_DT_BF16 || dt == BITNET_DT_F32; }
 
@@ -453,7 +455,8 @@ bitnet_status_t check(const FusedArgs &p, int gated) {
         (p.residual && (!at(p.residual, 16) || !float_type(p.rdt))) || !at(p.y, 16) || !float_type(p.ydt) ||
         p.act < BITNET_ACT_NONE || p.act > BITNET_ACT_GELU || (p.residual == p.y && p.rdt != p.ydt))
         return BITNET_ERR_INVALID_ARG;
-    if (bitnet_check_shape(p.N, p.K) != BITNET_OK || (gated && p.N % 32)) return BITNET_ERR_UNSUPPORTED_SHAPE;
+    if (bitnet_check_shape(p.N, p.K) != BITNET_OK || (gated && p.N % 32) || p.K > kMostK || (int64_t)p.N * p.K > kMostWeights)
+        return BITNET_ERR_UNSUPPORTED_SHAPE;
     return BITNET_OK;
 }
 

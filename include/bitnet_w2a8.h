@@ -593,7 +593,9 @@ typedef enum {
  *   y         device, ydt BITNET_DT_BF16 or BITNET_DT_F32 (out)
  * A token whose s_a is NaN has rows of NaN (the activations keep a NaN); other tokens do not see it.
  *   workspace  device, 16-byte aligned, >= bitnet_w2a8_linear_workspace_bytes(M, N, K); clobbered; may be NULL where that is 0
- * Rules: the shape rules, 1 <= M <= 2^24, N % 32 == 0 when gated. */
+ * y overlaps no other operand (but the residual that it is).
+ * Rules: the shape rules, K <= 2^24, N * K <= 2^34, 1 <= M <= 2^24, N % 32 == 0 when gated; where a workspace is needed M * K < 2^31
+ * and ceil(M / 64) * ceil(N / 256) <= 2^23. */
 size_t bitnet_w2a8_linear_workspace_bytes(int M, int N, int K);
 bitnet_status_t bitnet_w2a8_linear(const uint8_t *packed, const float *scales, const int8_t *q, const float *s_a,
                                    const float *bias, int act, int gated, const void *residual, int rdt, void *y,
@@ -632,7 +634,8 @@ bitnet_status_t bitnet_route(const void *logits, int dt, int64_t row_stride, int
  *   bias      device, fp32 [experts][N], or NULL
  *   y         device, [slots][N, or N/2 when gated] of ydt (out); rows of no expert are not written
  *   workspace  device, 16-byte aligned, >= bitnet_w2a8_grouped_workspace_bytes(...); clobbered; may be NULL where that is 0
- * Rules: as bitnet_w2a8_linear; 1 <= experts <= 1024; 1 <= slots, tokens <= 2^24; without rows tokens >= slots. */
+ * Rules: as bitnet_w2a8_linear (tokens in the place of M, a matrix's N and K; token tiles of 64 slots, one more an expert); 1 <= experts
+ * <= 1024; 1 <= slots, tokens <= 2^24; without rows tokens >= slots. */
 size_t bitnet_w2a8_grouped_workspace_bytes(int tokens, int slots, int experts, int N, int K);
 bitnet_status_t bitnet_w2a8_grouped(const uint8_t *packed, const float *scales, const int8_t *q, const float *s_a,
                                     int tokens, const int32_t *starts, const int32_t *rows, int experts, int slots,

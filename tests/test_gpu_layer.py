@@ -148,6 +148,14 @@ def test_norm_of_the_stored_stream(gpu):
     assert torch.equal(q, q2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("K", [4112, 8208, 8704, 16400, 32768, 32784])
+@pytest.mark.parametrize("parts", [0, 2])
+def test_norm_in_place_where_lanes_have_no_chunk(gpu, K, parts):
+    """x_out is x, and the row ends inside the lanes' last round: what another wave has stored meanwhile is not seen."""
+    for M in (1, 40):
+        _norm_case(np.random.default_rng(K + M), M, K, "fp32", "bf16", parts, inplace=True)
+
+
 # ------------------------------------------------------------------ products
 def _weights(rng, N, K):
     T = (rng.integers(0, 3, (N, K), dtype=np.int8) - 1).astype(np.int8)
@@ -242,6 +250,26 @@ def test_linear_of_a_token_that_is_not_finite(gpu, M):
             want, tol = lo.linear(T, S, q, s_a, None, act, gated, None, torch.float32)
         want[1] = np.nan
         lo.close(bn.PackedWeight.from_ternary(T, S).linear(_dev(q), _dev(s_a), act=act, gated=gated, out_dtype=torch.float32), want, tol)
+
+
+@pytest.mark.parametrize("M", [1, 9, 48, 49, 64, 300])
+def test_linear_whole_numbers_exactly(gpu, M):
+    """With scales and factors of one every output is a whole number below 2^24: all int8 codes, -128 among them, every column order,
+    the largest sums there are."""
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(M)
+    for N, K in ((272, 128), (32, 640), (544, 2560)):
+        T = (rng.integers(0, 3, (N, K), dtype=np.int8) - 1).astype(np.int8)
+        T[0], T[1] = 1, -1
+        T[2:18] = 0
+        T[2:18][np.arange(16), rng.integers(0, K, 16)] = 1  # a column alone
+        q = rng.integers(-128, 128, (M, K), dtype=np.int64).astype(np.int8)
+        q[0] = np.arange(K) % 256 - 128
+        q[-1] = -128 if M > 1 else q[-1]
+        if M > 2:
+            q[1] = 127
+        y = bn.PackedWeight.from_ternary(T, np.ones((N, K // 128), np.float32)).linear(_dev(q), _dev(np.ones(M, np.float32)), out_dtype=torch.float32)
+        assert np.array_equal(y.cpu().numpy(), (q.astype(np.int64) @ T.astype(np.int64).T).astype(np.float32))
 
 
 # ------------------------------------------------------------------ products by expert

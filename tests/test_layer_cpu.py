@@ -47,7 +47,7 @@ def test_linear_refusals():
     for kw in (dict(s_a=NULL), dict(s_a=MIS4), dict(bias=MIS), dict(residual=MIS), dict(act=-1), dict(act=5), dict(rdt=2), dict(ydt=-1),
                dict(ydt=2), dict(residual=P2)):
         assert _call(f, order, base, **kw) == ARG, kw
-    for kw in (dict(M=0), dict(M=-4), dict(M=(1 << 24) + 1), dict(N=0), dict(N=40), dict(N=-16), dict(K=64), dict(K=0), dict(gated=1), dict(N=1 << 30, K=1 << 20)):
+    for kw in (dict(M=0), dict(M=-4), dict(M=(1 << 24) + 1), dict(N=0), dict(N=40), dict(N=-16), dict(K=64), dict(K=0), dict(gated=1), dict(N=1 << 30, K=1 << 20), dict(N=16, K=(1 << 24) + 128), dict(N=1 << 20, K=1 << 15)):
         assert _call(f, order, base, **kw) == SHAPE, kw
 
 
