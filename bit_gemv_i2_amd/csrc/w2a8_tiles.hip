@@ -45,9 +45,10 @@ __device__ __forceinline__ uint32_t upper4(uint32_t q) {  // (q + 8) >> 4; its s
 }
 
 // One lane: 32 columns of a token.  Column order, in every 16: that of the codes' nibbles in a word, 0 8 1 9 2 10 3 11, 4 12 ...
+// The 48 bytes of a lane go through LDS, so that a wave stores whole kilobytes.
 __global__ __launch_bounds__(256) void digits_kernel(const int8_t *__restrict__ q, uint8_t *__restrict__ out, int64_t pieces) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= pieces) return;
+    __shared__ uint4 s_out[256 * 3];
+    const int64_t first = (int64_t)blockIdx.x * 256, i = min(first + threadIdx.x, pieces - 1);
     const uint4 x[2] = {reinterpret_cast<const uint4 *>(q)[2 * i], reinterpret_cast<const uint4 *>(q)[2 * i + 1]};
     uint32_t d[12];
 #pragma unroll
@@ -65,9 +66,15 @@ __global__ __launch_bounds__(256) void digits_kernel(const int8_t *__restrict__ 
             to[2] = (g[2] >> 16) | (g[3] << 8);
         }
     }
-    uint4 *to = reinterpret_cast<uint4 *>(out) + 3 * i;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) to[k] = make_uint4(d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]);
+    for (int k = 0; k < 3; ++k) s_out[3 * threadIdx.x + k] = make_uint4(d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]);
+    __syncthreads();
+    uint4 *to = reinterpret_cast<uint4 *>(out) + 3 * first;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int at = 256 * k + threadIdx.x;
+        if (first * 3 + at < pieces * 3) to[at] = s_out[at];
+    }
 }
 
 // --------------------------------------------------------------------------------------------- tiles
@@ -83,7 +90,7 @@ constexpr int kThreads = 256, kStages = 3, kTokens = 64;
 constexpr int kDigitStage = kTokens * kDigitRow, kWeightStage = 16 * 512, kScaleStage = 16 * 16 * 4;
 constexpr int kStage = kDigitStage + kWeightStage + kScaleStage;
 constexpr int kCUs = 256;
-constexpr int kBand = 8;  // token tiles that share the rows' tiles
+constexpr int kBand = 4;  // token tiles that share the rows' tiles
 
 // 16 bytes a lane from base + offset into LDS at lds + 16 * lane, the next kilobyte of LDS for each further load; M0 carries the
 // LDS address and is restored.
