@@ -39,7 +39,7 @@ __device__ __forceinline__ float activate(float z) {
 }
 
 // f(the activation as a type): one branch around an epilogue.  A branch at each value made the epilogue of a 64 x 256 tile 3.5 us long
-// where it now takes 0.6.
+// where it now takes 1.4.
 template <int ACT>
 struct Act {
     static constexpr int value = ACT;
@@ -95,7 +95,8 @@ __device__ __forceinline__ bool find_tile(const FusedArgs &p, int tile, int rows
     return false;
 }
 
-// The `rank`-th expert that has any rows, and all its slots.
+// The `rank`-th expert that has any rows, and all its slots.  By ballots and counts of bits: a scan by shuffles made a product of one
+// token with 2 of 8 experts 6.3 us long instead of 5.6.
 __device__ __forceinline__ bool find_expert(const FusedArgs &p, int rank, Tile *out) {
     const int lane = threadIdx.x & 63;
     for (int e0 = 0; e0 < p.experts; e0 += 64) {

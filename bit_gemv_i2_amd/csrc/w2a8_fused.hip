@@ -31,8 +31,13 @@ __device__ __forceinline__ v4i mfma_i8(v4i a, v4i b, v4i c) { return __builtin_a
 // so no barrier), multiplies, and the waves' sums are joined in LDS in a fixed order.  Further tokens of the expert, TOK at a
 // time, meet the codes still in registers.  By expert, workgroup row y has the y-th expert that has any rows, so that no
 // more than there are slots are launched.
+//
+// Floor: the weights once (9 bits of 32 a weight: 2560 x 6912 5 MB, 13824 x 2560 10 MB; 0.8 and 1.6 us at a bare read's 6.3 TB/s) and a
+// launch.  Measured in a graph, weights from HBM: 1 token x 2560 x 6912 4.1 us, 8 x 13824 x 2560 gated 5.7, 16 tokens 6.4, 1 x
+// 131072 x 2560 19.6 (4.8 TB/s).  What bounds it: few tiles, one workgroup's chain (launch, loads, products, join); many tiles, the
+// time in which a workgroup has no weights in flight (its start, join and end: half of some 4 us).
 // ==========================================================================
-constexpr int kMostWaves = 12;
+constexpr int kMostWaves = 12;  // 170 registers a lane, and 96 blocks before a wave has to take its blocks in turns
 
 struct RowsArgs {
     FusedArgs p;
@@ -89,11 +94,15 @@ __global__ __launch_bounds__(64 * kMostWaves) void rows_kernel(RowsArgs a) {
     v4i x[kLoads];
     auto load_x = [&](int c0) {
         const int o = min(l & (P - 1), min(NB, b1 - c0) * 8 - 1), safe = followed(token) ? token : 0;
-        const int8_t *from = p.q + c0 * 128 + o * 16;
+        const int8_t *from = p.q + c0 * 128;
 #pragma unroll
         for (int r = 0; r < kLoads; ++r) {
-            const int row = P == 64 ? __builtin_amdgcn_readlane(safe, r) : __shfl(safe, min(r * kTogether + l / P, TOK - 1));
-            x[r] = *reinterpret_cast<const v4i *>(from + (int64_t)row * p.K);
+            if (P == 64) {  // a base for all lanes and a lane's 32-bit offset
+                const int8_t *row = from + (int64_t)__builtin_amdgcn_readlane(safe, r) * p.K;
+                x[r] = *reinterpret_cast<const v4i *>(row + (uint32_t)(o * 16));
+            } else {
+                x[r] = *reinterpret_cast<const v4i *>(from + (int64_t)__shfl(safe, min(r * kTogether + l / P, TOK - 1)) * p.K + o * 16);
+            }
         }
     };
     // what the outputs of a pass need at their end: output tid + r * threads is token (..) / 16, row (..) % 16
@@ -125,6 +134,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void rows_kernel(RowsArgs a) {
                 const v4i q0 = *reinterpret_cast<const v4i *>(op + i * 128), q1 = *reinterpret_cast<const v4i *>(op + i * 128 + 64);
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
+                    asm("" : "+v"(code[h][i].x), "+v"(code[h][i].y));  // decoded again in each pass, not kept four times as large across them
                     v4i c = mfma_i8(q0, decode16(code[h][i].x), v4i{0, 0, 0, 0});
                     c = mfma_i8(q1, decode16(code[h][i].y), c);
 #pragma unroll
@@ -346,7 +356,9 @@ __global__ __launch_bounds__(256) void stream_kernel(StreamArgs a) {
     }
 }
 
-constexpr int kStreamWaves = 4096, kStreamFrom = 1024;  // waves of a launch; tiles of 16 rows from which on it is used
+// Waves of a launch (64 experts of 2560 x 1280: 6 rows an expert 17.6 us, with 2048 19.3, with 8192 19.9; 12 rows 24.6, 28.9 and 26.0), and the
+// tiles of 16 rows from which on it is used: as many as the chip holds workgroups of it.
+constexpr int kStreamWaves = 4096, kStreamFrom = 1024;
 
 template <bool GATED, int NB>
 void launch_stream_nb(const StreamArgs &a, dim3 grid, size_t lds, hipStream_t stream) {
@@ -376,23 +388,22 @@ bool launch_stream(const FusedArgs &p, hipStream_t stream) {
     return true;
 }
 
-constexpr int kMostLds = 65536;
-constexpr int kCUs = 256, kWaveSlots = kCUs * 32;
+constexpr int kMostLds = 163840, kCUs = 256;
+
+int blocks_held(int per) { return per <= 2 ? 2 : per <= 4 ? 4 : per <= 8 ? per : 8; }  // of a wave's: the NB below
 
 template <bool GATED, bool GROUPED, int TOK>
 void launch_rows_tok(const RowsArgs &a, dim3 grid, hipStream_t stream) {
     const dim3 block(64 * a.waves);
-    const int nb = a.per <= 6 ? a.per : 8;
-    const size_t lds = (size_t)a.waves * (TOK * (nb * 128 + 16) + (GATED ? 2 : 1) * 1024);
+    const size_t lds = (size_t)a.waves * (TOK * (blocks_held(a.per) * 128 + 16) + (GATED ? 2 : 1) * 1024);
 #define BITNET_ROWS(NB, MULTI) hipLaunchKernelGGL((rows_kernel<GATED, GROUPED, NB, TOK, MULTI>), grid, block, lds, stream, a)
     switch (a.per) {
-        case 1: BITNET_ROWS(1, false); return;
-        case 2: BITNET_ROWS(2, false); return;
-        case 3: BITNET_ROWS(3, false); return;
-        case 4: BITNET_ROWS(4, false); return;
+        case 1: case 2: BITNET_ROWS(2, false); return;
+        case 3: case 4: BITNET_ROWS(4, false); return;
         case 5: BITNET_ROWS(5, false); return;
         case 6: BITNET_ROWS(6, false); return;
-        case 7: case 8: BITNET_ROWS(8, false); return;
+        case 7: BITNET_ROWS(7, false); return;
+        case 8: BITNET_ROWS(8, false); return;
         default: BITNET_ROWS(8, true);
     }
 #undef BITNET_ROWS
@@ -411,32 +422,42 @@ void run_rows(const FusedArgs &p, int gated, hipStream_t stream) {
     const int some = p.starts ? (p.experts < p.slots ? p.experts : p.slots) : 1;  // experts that can have rows
     const int64_t work = (int64_t)tiles * some;
     const int usual = (p.slots + some - 1) / some;
+    // 64 experts of 2560 x 1280: 2 rows an expert 17.6 us against the rows kernel's 16.5, 6 rows 18.4 against 25.1, 12 rows 24.1 against 33.0;
+    // 8 of 6912 x 2560: 4 rows 13.4 against 12.8, 8 rows 14.7 against 14.8.
     if (p.starts && usual > 4 && work >= kStreamFrom && (gated ? launch_stream<true>(p, stream) : launch_stream<false>(p, stream))) return;
+    // Tokens of a pass: a pass reads them whether they are there or not, but two passes cost more than one of twice as many. 13824 x 2560 gated, in
+    // passes of 1, 4, 8 and 16 tokens: 1 token 4.9, 5.2, 5.6, 6.2 us; 4 tokens 9.1, 5.2, 5.7, 6.2; 8 tokens 14.7, 7.0, 5.7, 6.4;
+    // 12 tokens 20.3, 8.8, 8.0, 6.4.
     int tok = usual == 1 ? 1 : usual <= 4 ? 4 : usual <= 8 ? 8 : 16;
-    int per = gated ? 2 : 4;
-    auto waves = [&](int n) { return (blocks + n - 1) / n; };
-    if (waves(per) > kMostWaves) per = waves(kMostWaves);
-    while (per < 8 && per < blocks && work * waves(per) > kWaveSlots) ++per;
-    if (per > blocks) per = blocks;
-    if (work <= kCUs && blocks >= 8 && per <= 8) {  // a workgroup a CU: as long as the busiest of its four SIMDs
-        int best = (waves(per) + 3) / 4 * per;
-        for (int n = 8; n >= 1; --n)
-            if (waves(n) <= kMostWaves && (waves(n) + 3) / 4 * n < best) best = (waves(n) + 3) / 4 * n, per = n;
-    }
-    a.waves = waves(per);
-    a.per = per = waves(a.waves);  // evenly
-    // the tokens' slices have to fit 64 KiB beside the sums
-    while (tok > 4 && a.waves * (tok * ((per <= 6 ? per : 8) * 128 + 16) + (gated ? 2 : 1) * 1024) > kMostLds) tok >>= 1;
+    auto over = [&](int n) { return (blocks + n - 1) / n; };
+    // Waves in fours, so that the SIMDs have as many each, of 4 to 8 blocks: 8 x 13824 x 2560 gated 5.7 us with 4 waves, 6.1 with 3, 5.9 with 5,
+    // 7.0 with 10; 8 x 20480 x 3200 7.9 with 4, 9.6 with 5, 9.2 with 7; 16 x 2560 x 6912 5.6 with 8, 7.0 with 4, 6.1 with 11.  Two for
+    // short columns: 64 experts of 2560 x 1280 16.0 with 2, 20.8 with 4.
+    a.waves = blocks > 12 ? min((over(8) + 3) / 4 * 4, kMostWaves) : blocks > 3 ? 2 : 1;
+    a.per = over(a.waves);
+    a.waves = over(a.per);
+    // All of LDS for tokens, even where it leaves one workgroup a CU: 16 x 2560 x 6912 5.6 us (141 KB), in passes of 8 tokens 7.0; 16 x 13824 x
+    // 8192 gated 14.3 and 21.1.
+    while (tok > 4 && a.waves * (tok * (blocks_held(a.per) * 128 + 16) + (gated ? 2 : 1) * 1024) > kMostLds) tok >>= 1;
     const dim3 grid((unsigned)tiles, (unsigned)some);
     if (p.starts) gated ? launch_rows<true, true>(a, tok, grid, stream) : launch_rows<false, true>(a, tok, grid, stream);
     else gated ? launch_rows<true, false>(a, tok, grid, stream) : launch_rows<false, false>(a, tok, grid, stream);
 }
 
-// Whether the tiles of w2a8_tiles.hip take it, by the rows of an expert on the average.
-bool many(int64_t slots, int experts, bool grouped) { return grouped ? slots > 16ll * experts : slots > 48; }
+// Whether the tiles of w2a8_tiles.hip take it.
+//     By expert (rows or stream against tiles): 12 rows, 64 experts of 2560 x 1280 24.1 us against 31.6, 24 rows 39.8 against 34.4; 16 rows, 8 experts
+// of 6912 x 2560 22.6 against 20.4, of 2560 x 6912 32.5 against 32.6, 32 rows 30.8 against 26.9 and 46.3 against 33.1.
+//     Else by passes of 16 tokens and tiles of 16 rows a CU, which is what rows cost, while tiles of this few tokens take the time of one chain over
+// K: 2560 x 2560 64 tokens 9.5 us against 17.0, 128 17.0 against 17.5; 13824 x 2560 gated 64 15.7 against 17.0, 80 18.3 against 16.8; 20480 x
+// 3200 32 17.9 against 19.4, 40 24.8 against 19.7; 65536 x 2560 32 37.4 against 23.2; 2560 x 6912 128 26.7 against 31.8.
+bool many(int64_t slots, int experts, bool grouped, int N) {
+    if (grouped) return slots > 16ll * experts;
+    const int64_t passes = (slots + 15) / 16;
+    return passes > 1 && passes * max(N / 16, 2 * kCUs) > 14 * kCUs;
+}
 
 bitnet_status_t run(const FusedArgs &p, int gated, void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    if (many(p.slots, p.experts, p.starts)) {
+    if (many(p.slots, p.experts, p.starts, p.N)) {
         if (!at(workspace, 16) || workspace_bytes < digits_bytes(p.tokens, p.K)) return BITNET_ERR_INVALID_ARG;
         return launch_tiles(p, gated, workspace, stream);
     }
@@ -465,7 +486,7 @@ bitnet_status_t check(const FusedArgs &p, int gated) {
 extern "C" {
 
 size_t bitnet_w2a8_linear_workspace_bytes(int M, int N, int K) {
-    return M < 1 || bitnet_check_shape(N, K) != BITNET_OK || !many(M, 1, false) ? 0 : digits_bytes(M, K);
+    return M < 1 || bitnet_check_shape(N, K) != BITNET_OK || !many(M, 1, false, N) ? 0 : digits_bytes(M, K);
 }
 
 bitnet_status_t bitnet_w2a8_linear(const uint8_t *packed, const float *scales, const int8_t *q, const float *s_a,
@@ -480,7 +501,7 @@ bitnet_status_t bitnet_w2a8_linear(const uint8_t *packed, const float *scales, c
 }
 
 size_t bitnet_w2a8_grouped_workspace_bytes(int tokens, int slots, int experts, int N, int K) {
-    return tokens < 1 || slots < 1 || experts < 1 || bitnet_check_shape(N, K) != BITNET_OK || !many(slots, experts, true) ? 0 : digits_bytes(tokens, K);
+    return tokens < 1 || slots < 1 || experts < 1 || bitnet_check_shape(N, K) != BITNET_OK || !many(slots, experts, true, N) ? 0 : digits_bytes(tokens, K);
 }
 
 bitnet_status_t bitnet_w2a8_grouped(const uint8_t *packed, const float *scales, const int8_t *q, const float *s_a,

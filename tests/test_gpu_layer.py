@@ -219,6 +219,18 @@ def test_linear_wide(gpu, M, N, K, gated):
     _linear_case(np.random.default_rng(M + N), M, N, K, "relu2" if gated else "none", gated, N % 3 == 0, "bf16" if M % 2 else None, "bf16")
 
 
+@pytest.mark.parametrize("blocks", [4, 6, 10, 13, 16, 17, 24, 25, 32, 33, 48, 64, 65, 96, 130])
+@pytest.mark.parametrize("M", [1, 4, 8, 12, 16, 37])
+def test_linear_few_rows_of_long_columns(gpu, blocks, M):
+    _linear_case(np.random.default_rng(blocks * M), M, 64, 128 * blocks, "relu2", blocks % 2 == 1, blocks % 3 == 0, "bf16", "fp32")
+
+
+@pytest.mark.parametrize("M,N", [(112, 96), (113, 96), (64, 14016), (65, 14016), (32, 20480), (33, 20480), (16, 65536), (17, 65536)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_between_few_rows_and_many(gpu, M, N, gated):
+    _linear_case(np.random.default_rng(M), M, N, 256, "silu", gated, True, "fp32", "bf16")
+
+
 @pytest.mark.parametrize("out", list(TYPES))
 @pytest.mark.parametrize("M", [1, 16, 90, 300])
 def test_linear_into_its_residual(gpu, out, M):

@@ -72,6 +72,10 @@ def test_product_workspaces():
     assert bn.lib().bitnet_w2a8_linear_workspace_bytes(4000, 32, 256) == 4000 * 2 * 192
     assert bn.lib().bitnet_w2a8_linear_workspace_bytes(1 << 24, 32, 256) == (1 << 24) * 2 * 192
     assert bn.lib().bitnet_w2a8_grouped_workspace_bytes(4000, 8000, 8, 32, 256) == 4000 * 2 * 192
+    for M in (1, 16, 17, 48, 112):
+        assert bn.lib().bitnet_w2a8_linear_workspace_bytes(M, 2560, 2560) == 0
+    assert bn.lib().bitnet_w2a8_linear_workspace_bytes(113, 2560, 2560) == 113 * 20 * 192
+    assert bn.lib().bitnet_w2a8_linear_workspace_bytes(16, 1 << 20, 256) == 0 < bn.lib().bitnet_w2a8_linear_workspace_bytes(17, 1 << 20, 256)
     assert bn.lib().bitnet_w2a8_grouped_workspace_bytes(40, 80, 80, 32, 256) == 0
     for bad in ((0, 32, 256), (4000, 40, 256), (4000, 32, 100)):
         assert bn.lib().bitnet_w2a8_linear_workspace_bytes(*bad) == 0
