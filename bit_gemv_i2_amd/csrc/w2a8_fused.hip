@@ -3,7 +3,7 @@
 //     z[m][n] = s_a[m] * sum_b S[n][b] * A[m][n][b] + bias[n],   y = act(z) (+ residual),  gated: act(z_gate) * z_up
 //
 // on the int8 matrix cores, as the products without an epilogue: lane (g, j) of a wave supplies row j of 16 weight rows
-// and token j of 16 tokens at 16 columns 16 g + 64 s, and receives rows 4g .. 4g + 3 of token j, so that bias, activation
+// and token j of 16 tokens at 16 columns 16 g + 64 s, and receives tokens 4g .. 4g + 3 of row j, so that bias, activation
 // and residual are a lane's own and the gate and the up projection of an output meet in one lane.
 #include "fused.h"
 

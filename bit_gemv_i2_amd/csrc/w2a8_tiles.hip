@@ -367,8 +367,7 @@ __global__ __launch_bounds__(kThreads * KS, 2) void tiles_kernel(FusedArgs p, co
 template <bool GATED>
 bitnet_status_t launch(const FusedArgs &p, const uint8_t *digits, hipStream_t stream) {
     const int64_t tiles = token_tiles(p, kTokens);
-    const int row_tiles = GATED ? (p.N / 32 + 7) / 8 : (p.N / 16 + 15) / 16;
-    if (tiles * row_tiles > (1 << 23)) return BITNET_ERR_UNSUPPORTED_SHAPE;  // the launch's work items in 32 bits
+    const int row_tiles = (p.N + 255) / 256;
     constexpr int out_bytes = kTokens * ((GATED ? 128 : 256) + 4) * 4, stages = kStages * kStage;
     const dim3 grid((unsigned)(tiles * row_tiles));
     if (tiles * row_tiles <= kCUs) hipLaunchKernelGGL((tiles_kernel<GATED, 2>), grid, dim3(2 * kThreads), 2 * stages, stream, p, digits, row_tiles, (int)tiles);
@@ -385,6 +384,7 @@ size_t digits_bytes(int tokens, int K) { return (size_t)tokens * (size_t)(K / 12
 bitnet_status_t launch_tiles(const FusedArgs &p, int gated, void *digits, hipStream_t stream) {
     const int64_t pieces = (int64_t)p.tokens * (p.K / 32);
     if ((int64_t)p.tokens * p.K > INT32_MAX) return BITNET_ERR_UNSUPPORTED_SHAPE;  // 1.5 bytes a value: offsets in 32 bits
+    if (token_tiles(p, kTokens) * (((int64_t)p.N + 255) / 256) > (1 << 23)) return BITNET_ERR_UNSUPPORTED_SHAPE;  // the launch's work items in 32 bits
     hipLaunchKernelGGL(digits_kernel, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, stream, p.q, static_cast<uint8_t *>(digits), pieces);
     return gated ? launch<true>(p, static_cast<const uint8_t *>(digits), stream) : launch<false>(p, static_cast<const uint8_t *>(digits), stream);
 }

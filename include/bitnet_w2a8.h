@@ -619,7 +619,8 @@ bitnet_status_t bitnet_w2a8_linear(const uint8_t *packed, const float *scales, c
  *   rows     device, int32 [tokens * k] (out): the token of every slot, -1 behind the last one
  *   slots    device, int32 [tokens][k] (out): the slot of every assignment, or -1
  *   workspace  device, 16-byte aligned, >= bitnet_route_workspace_bytes(...); clobbered; may be NULL where that is 0
- * Rules: 1 <= k <= 32, k <= experts <= 1024, tokens >= 1, tokens * k <= 2^30; row_stride >= experts.  Outputs do not overlap. */
+ * Rules: 1 <= k <= 32, k <= experts <= 1024, tokens >= 1, tokens * k <= 2^30; experts <= row_stride <= 2^31.  Outputs do not
+ * overlap. */
 size_t bitnet_route_workspace_bytes(int tokens, int experts, int k);
 bitnet_status_t bitnet_route(const void *logits, int dt, int64_t row_stride, int tokens, int experts, int k,
                              int over_all, int32_t *chosen, float *gates, int32_t *starts, int32_t *rows,

@@ -87,6 +87,10 @@ def test_product_workspaces():
         assert f(P, P, P, P, NULL, 0, 0, NULL, 0, P2, F32, 4000, 32, 256, ws, nb, NULL) == ARG
     for ws, nb in ((NULL, 0), (P, need - 1), (MIS, need)):
         assert bn.lib().bitnet_w2a8_grouped(P, P, P, P, 4000, P, P, 2, 4000, NULL, 0, 0, P2, F32, 32, 256, ws, nb, NULL) == ARG
+    # digits past 32 bits of offset, and more tiles than a launch holds
+    for M, N, K in ((1 << 24, 32, 128), (1 << 17, 32, 1 << 14), (1 << 20, 1 << 19, 128)):
+        assert f(P, P, P, P, NULL, 0, 0, NULL, 0, P2, F32, M, N, K, P, M * (K // 128) * 192, NULL) == SHAPE
+        assert bn.lib().bitnet_w2a8_grouped(P, P, P, P, M, P, P, 1, 1 << 20, NULL, 0, 0, P2, F32, N, K, P, M * (K // 128) * 192, NULL) == SHAPE
 
 
 def test_route_refusals():
