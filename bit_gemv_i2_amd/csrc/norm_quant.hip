@@ -349,7 +349,8 @@ extern "C" bitnet_status_t bitnet_add_norm(const void *x, int xdt, const void *a
         (!slots && (gates || parts)) || (!q && !h_out) || (q && (!at(q, 16) || !at(s_a, 4))) || (!q && s_a) ||
         (h_out && (!at(h_out, 16) || !float_type(hdt))) || !(eps > 0.0f) || !std::isfinite(eps))
         return BITNET_ERR_INVALID_ARG;
-    if (M < 1 || M > 65535 * 1024 || K < 16 || K % 16 || K > kMaxK ||
+    // a launch's work items in 32 bits: 64 a row, or up to 1024 (launch_norm)
+    if (M < 1 || M > 65535 * 1024 || (M >= 1 << 22 && K > (slots ? 512 : 4096)) || K < 16 || K % 16 || K > kMaxK ||
         (slots && (parts < 1 || parts > kMaxParts || add_rows < 1)))
         return BITNET_ERR_UNSUPPORTED_SHAPE;
     NormArgs p;

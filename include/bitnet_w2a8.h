@@ -565,7 +565,8 @@ bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, const void *
  *   h_out    device, [M][K], hdt BITNET_DT_BF16 or BITNET_DT_F32 (out), or NULL
  * A row whose h holds an infinity or a NaN (of x, add, a gate or the weight) has s_a = NaN and codes of 0, so that
  * every product of it is NaN; other rows do not see it.
- * Rules: M >= 1; 16 <= K <= 65536, K % 16 == 0; with slots 1 <= parts <= 64 and add_rows >= 1; eps > 0 and finite; one of q and
+ * Rules: 1 <= M <= 65535 * 1024, and below 2^22 where K > 4096 or, with slots, K > 512; 16 <= K <= 65536, K % 16 == 0; with slots
+ * 1 <= parts <= 64 and add_rows >= 1; eps > 0 and finite; one of q and
  * h_out at least. */
 bitnet_status_t bitnet_add_norm(const void *x, int xdt, const void *add, int adt, int64_t add_rows,
                                 const int32_t *slots, const float *gates, int parts, const float *weight, float eps,

@@ -33,7 +33,7 @@ def test_add_norm_refusals():
                dict(eps=0.0), dict(eps=-1e-5), dict(eps=math.inf), dict(eps=math.nan), dict(eps=1e-60)):
         assert _call(bn.lib().bitnet_add_norm, order, base, **kw) == ARG, kw
     for kw in (dict(M=0), dict(M=-1), dict(M=65535 * 1024 + 1), dict(K=0), dict(K=-16), dict(K=24), dict(K=65552), dict(parts=0), dict(parts=-1),
-               dict(parts=65), dict(add_rows=0), dict(add_rows=-3)):
+               dict(parts=65), dict(add_rows=0), dict(add_rows=-3), dict(M=1 << 22, K=528), dict(M=1 << 22, K=4112, slots=NULL, gates=NULL, parts=0)):
         assert _call(bn.lib().bitnet_add_norm, order, base, **kw) == SHAPE, kw
 
 
