@@ -13,8 +13,8 @@
 // layout come out of their words.
 //
 // Measured, digits and products together: 8192 tokens x 6912 x 2560, gated, 165 to 175 us, 1.66 to 1.76 POP/s (the plain product's
-// kernel 192 to 198 us; a large int8 library product runs at 2.55 POP/s); 512 x 13824 x 2560 30 us (30); 256 rows 19.5
-// (21.7).  Four steps a 32 x 32 block, two digits each of two halves, are what int8 takes too.  What bounds it with many tiles is the
+// kernel 192 to 198 us; a large int8 library product runs at 2.55 POP/s); 512 x 13824 x 2560 30 us (30), 256
+// tokens 19.5 (21.7).  Four steps a 32 x 32 block, two digits each of two halves, are what int8 takes too.  What bounds it with many tiles is the
 // matrix cores' clock and issue: a step is 14.3 ns with 32 workgroups on the card and 20 to 23 with all 512, whatever else the
 // waves do; of 4095 tokens' 357 thousand cycles the cores are busy in 40%, a wave waits for its turn in 32%, for
 // data or the barrier in 24%; LDS has no bank conflicts.  With few tiles it is one workgroup's chain of blocks, prologue and
@@ -94,8 +94,8 @@ __global__ __launch_bounds__(256) void digits_kernel(const int8_t *__restrict__ 
 // reads over all banks.  A wave works on one of its two row tiles at a time: under each of the 8 steps of it, it drains four sums
 // of the other (finished) row tile into fp32 with their scale, and makes words of that row tile's weights.
 // KS = 2, where the tiles are no more than the CUs: one workgroup of 8 waves a CU, the second four take every other block and
-// their sums are added once at the end (64 tokens x 13824 x 2560 gated 16.7 instead of 17.7 us, 512 x 2560 x 6912 35.6 instead of
-// 39.6).  With more tiles than CUs the two workgroups of a CU are that already.
+// their sums are added once at the end (512 x 2560 x 6912 35.6 us instead of 39.6, 64 x 13824 x 2560 gated
+// 16.7 instead of 17.7).  With more tiles than CUs the two workgroups of a CU are that already.
 constexpr int kThreads = 256, kStages = 3, kTokens = 64;
 constexpr int kDigitStage = kTokens * kDigitRow, kWeightStage = 16 * 512, kScaleStage = 16 * 16 * 4;
 constexpr int kStage = kDigitStage + kWeightStage + kScaleStage;
