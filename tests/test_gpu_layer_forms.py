@@ -1,0 +1,105 @@
+"""The forms of the operators between a decoder layer's products that a launch takes at sizes of its own: tiles beyond one round of
+compute units, streams of weights through several row tiles, columns taken in turns, rows of a norm on a wave each.  Oracles and
+tolerances are those of layer_oracle."""
+import numpy as np
+import pytest
+
+import layer_oracle as lo
+import test_gpu_layer as layer
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+# ------------------------------------------------------------------ tiles: more of them than compute units (256)
+def _tiles(M, N):
+    return -(-M // 64) * -(-N // 256)
+
+
+@pytest.mark.parametrize("M,N", [(1024, 4096), (1025, 4096), (16384, 256), (16385, 256), (64, 65536), (65, 65536)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_on_either_side_of_the_compute_units(gpu, M, N, gated):
+    assert (_tiles(M, N) > 256) == (M % 2 == 1)
+    layer._linear_case(np.random.default_rng(M), M, N, 128, "relu", gated, True, "fp32", "bf16")
+
+
+@pytest.mark.parametrize("act", lo.ACTS)
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_many_tiles_activations(gpu, act, gated):
+    i = lo.ACTS.index(act)
+    M, N = 1087 + i, 4128  # a last token tile that is not full, row tiles of which the last has 32 rows
+    assert _tiles(M, N) > 256
+    layer._linear_case(np.random.default_rng(i), M, N, 384, act, gated, i % 2 == 0, (None, "bf16", "fp32")[i % 3], ("bf16", "fp32")[i % 2])
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 3, 4, 5, 6, 7, 11])
+@pytest.mark.parametrize("M,N", [(1217, 4112), (1281, 4064)])
+def test_linear_many_tiles_blocks(gpu, blocks, M, N):
+    """Every stage of the loads in turn; bands of four token tiles of which the last has fewer."""
+    assert _tiles(M, N) > 256
+    layer._linear_case(np.random.default_rng(blocks), M, N, 128 * blocks, "none", False, blocks % 2 == 0, "bf16" if blocks % 3 else None, "fp32")
+
+
+@pytest.mark.parametrize("out", list(layer.TYPES))
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_many_tiles_into_the_residual(gpu, out, gated):
+    layer._linear_case(np.random.default_rng(1), 1100, 4160, 256, "silu" if gated else "none", gated, True, out, out, inplace=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(1090, 4128, 640), (16450, 272, 256)])
+def test_linear_many_tiles_whole_numbers_exactly(gpu, M, N, K):
+    import bit_gemv_i2_amd as bn
+    assert _tiles(M, N) > 256
+    rng = np.random.default_rng(M)
+    T = (rng.integers(0, 3, (N, K), dtype=np.int8) - 1).astype(np.int8)
+    T[0], T[1] = 1, -1
+    T[2:18] = 0
+    T[2:18][np.arange(16), rng.integers(0, K, 16)] = 1  # a column alone
+    q = rng.integers(-128, 128, (M, K), dtype=np.int64).astype(np.int8)
+    q[0], q[1], q[-1] = np.arange(K) % 256 - 128, 127, -128
+    w = bn.PackedWeight.from_ternary(T, np.ones((N, K // 128), np.float32))
+    y = w.linear(layer._dev(q), layer._dev(np.ones(M, np.float32)), out_dtype=torch.float32)
+    assert np.array_equal(y.cpu().numpy(), q.astype(np.float32) @ T.astype(np.float32).T)  # sums below 2^24: exact in any order
+
+
+def test_linear_many_tiles_of_a_token_that_is_not_finite(gpu):
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(4)
+    M, N, K = 1100, 4128, 256
+    T, S = layer._weights(rng, N, K)
+    q, s_a = layer._acts(rng, M, K)
+    bad = [1, 64, 700, M - 1]
+    s_a[bad], q[bad] = np.nan, 0
+    for act, gated in (("none", False), ("relu2", True)):
+        want, tol = lo.linear(T, S, q, np.where(np.isnan(s_a), 1, s_a).astype(np.float32), None, act, gated, None, torch.float32)
+        want[bad] = np.nan
+        lo.close(bn.PackedWeight.from_ternary(T, S).linear(layer._dev(q), layer._dev(s_a), act=act, gated=gated, out_dtype=torch.float32), want, tol)
+
+
+@pytest.mark.parametrize("counts", [[300, 0, 517, 64, 1, 190], [1100], [0, 0, 1200, 0], [65] * 20, [1] * 63 + [1400]])
+@pytest.mark.parametrize("gated,gather", [(False, False), (True, True)])
+def test_grouped_many_tiles(gpu, counts, gated, gather):
+    slots, some = sum(counts), min(len(counts), sum(counts))
+    N = 4128 if len(counts) < 20 else 2080
+    assert slots > 16 * len(counts) and (slots + 63 * some) // 64 * -(-N // 256) > 256
+    layer._grouped_case(np.random.default_rng(slots), counts, 333, N, 128, "silu" if gated else "none", gated, gated, gather, "bf16" if gated else "fp32")
+
+
+def test_grouped_many_tiles_bad_rows_and_rows_of_no_expert_stay(gpu):
+    layer._grouped_case(np.random.default_rng(5), [700, 0, 405], 90, 4128, 256, "none", False, True, True, "fp32", slots=1300,
+                        bad=[(0, -1), (2, 90), (699, -2 ** 31), (700, 2 ** 31 - 1), (1104, -7), (1200, 2 ** 31 - 1)])
+
+
+def test_grouped_many_tiles_starts_beyond_the_slots(gpu):
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(6)
+    layer._grouped_case(rng, [300, 5000, 9], 90, 4128, 128, "none", False, False, True, "fp32", slots=1100)
+    E, N, slots = 3, 4128, 1100
+    T, S = layer._weights(rng, E * N, 128)
+    w = bn.PackedExperts.from_ternary(T.reshape(E, N, 128), S.reshape(E, N, 1))
+    q, s_a = layer._acts(rng, slots, 128)
+    for starts in ([-5, 200, 400, 1 << 30], [1100, 200, 100, 0], [2 ** 31 - 1] * 4, [-2 ** 31, -1, -1, 2 ** 31 - 1], [0, 1100, 200, 1100]):
+        y, ok = layer._guarded((slots, N), torch.float32)
+        w.grouped(layer._dev(q), layer._dev(s_a), layer._dev(np.array(starts, np.int32)), y=y)
+        torch.cuda.synchronize()
+        assert ok()
