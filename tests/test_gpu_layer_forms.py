@@ -103,3 +103,97 @@ def test_grouped_many_tiles_starts_beyond_the_slots(gpu):
         w.grouped(layer._dev(q), layer._dev(s_a), layer._dev(np.array(starts, np.int32)), y=y)
         torch.cuda.synchronize()
         assert ok()
+
+
+# ------------------------------------------------------------------ few rows each of many experts
+def _ragged(E, usual):
+    """About `usual` rows an expert, some with none, one, a pass of 16 and more than one."""
+    counts = [usual] * E
+    for e, n in ((0, 0), (3, 1), (5, 16), (6, 17), (9, 37), (E - 1, usual + 2)):
+        counts[e] = n
+    assert 4 * E < sum(counts) <= 16 * E
+    return counts
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 13, 20, 31, 32])
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_stream_blocks(gpu, blocks, gated):
+    """Every chunk length and remainder; from 32 blocks on the rows no longer fit and another form takes over."""
+    E, N = 64, 512
+    assert N // (32 if gated else 16) * E >= 1024
+    layer._grouped_case(np.random.default_rng(blocks), _ragged(E, 5), 41, N, 128 * blocks, "relu2" if gated else "none", gated, blocks % 2 == 0,
+                        True, "fp32" if blocks % 3 else "bf16")
+
+
+@pytest.mark.parametrize("E,N,gated", [(64, 1296, False), (64, 1328, False), (64, 2592, True), (64, 2720, True), (16, 4208, False), (1024, 16, False),
+                                       (513, 64, True)])
+@pytest.mark.parametrize("usual", [5, 12])
+def test_grouped_stream_row_tiles(gpu, E, N, gated, usual):
+    """Several row tiles a wave, waves that have fewer or none, many experts."""
+    assert N // (32 if gated else 16) * E >= 1024
+    layer._grouped_case(np.random.default_rng(N), _ragged(E, usual), 97, N, 256 if E == 64 else 128, "silu", gated, usual == 5, usual == 12, "fp32")
+
+
+@pytest.mark.parametrize("act", lo.ACTS)
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_stream_activations(gpu, act, gated):
+    layer._grouped_case(np.random.default_rng(7), _ragged(64, 6), 50, 544, 384, act, gated, True, False, "bf16")
+
+
+def test_grouped_stream_bad_rows_and_rows_of_no_expert_stay(gpu):
+    counts = _ragged(64, 8)
+    used = sum(counts)
+    layer._grouped_case(np.random.default_rng(8), counts, 30, 512, 640, "none", False, True, True, "fp32", slots=used + 40,
+                        bad=[(0, -1), (2, 30), (17, 2 ** 31 - 1), (used - 1, -2 ** 31), (used + 1, 2 ** 31 - 1)])
+
+
+def test_grouped_stream_of_a_token_that_is_not_finite(gpu):
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(9)
+    E, N, K, usual = 64, 512, 384, 6
+    T, S = layer._weights(rng, E * N, K)
+    q, s_a = layer._acts(rng, E * usual, K)
+    bad = [1, 100, E * usual - 1]
+    s_a[bad], q[bad] = np.nan, 0
+    starts = np.arange(E + 1, dtype=np.int32) * usual
+    got = bn.PackedExperts.from_ternary(T.reshape(E, N, K), S.reshape(E, N, -1)).grouped(layer._dev(q), layer._dev(s_a), layer._dev(starts), out_dtype=torch.float32)
+    safe = np.where(np.isnan(s_a), 1, s_a).astype(np.float32)
+    for e in range(E):
+        at = slice(starts[e], starts[e + 1])
+        want, tol = lo.linear(T[e * N: (e + 1) * N], S[e * N: (e + 1) * N], q[at], safe[at], None, "none", False, None, torch.float32)
+        want[np.isnan(s_a[at])] = np.nan
+        lo.close(got[at], want, tol)
+
+
+def test_grouped_stream_starts_beyond_the_slots(gpu):
+    import bit_gemv_i2_amd as bn
+    rng = np.random.default_rng(10)
+    E, N, slots = 64, 512, 400
+    T, S = layer._weights(rng, E * N, 128)
+    w = bn.PackedExperts.from_ternary(T.reshape(E, N, 128), S.reshape(E, N, 1))
+    q, s_a = layer._acts(rng, slots, 128)
+    for starts in (np.linspace(-50, 1 << 30, E + 1), np.linspace(slots, 0, E + 1), np.full(E + 1, 2 ** 31 - 1), np.resize([0, slots, 9, slots], E + 1)):
+        y, ok = layer._guarded((slots, N), torch.float32)
+        w.grouped(layer._dev(q), layer._dev(s_a), layer._dev(starts.astype(np.int32)), y=y)
+        torch.cuda.synchronize()
+        assert ok()
+
+
+@pytest.mark.parametrize("E,slots,hot", [(64, 900, 450), (64, 1024, 960), (8, 128, 120)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_one_expert_with_most_of_the_rows(gpu, E, slots, hot, gated):
+    """Few rows an expert in the mean, many of one."""
+    counts = [0] * E
+    counts[2] = hot
+    for i in range(slots - hot):
+        counts[(5 * i + 7) % E if E == 8 else 3 + i % (E - 3)] += 1
+    assert slots == sum(counts) <= 16 * E
+    layer._grouped_case(np.random.default_rng(hot), counts, 80, 576, 384, "gelu", gated, False, True, "bf16")
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 1], [3, 5, 1], [7, 2, 9], [16, 0, 14], [4, 40, 3]])
+@pytest.mark.parametrize("blocks", [97, 110])
+def test_grouped_columns_in_turns(gpu, counts, blocks):
+    """More blocks of columns than the waves hold at once."""
+    for gated in (False, True):
+        layer._grouped_case(np.random.default_rng(blocks), counts, 11, 64, 128 * blocks, "relu", gated, True, gated, "fp32")
