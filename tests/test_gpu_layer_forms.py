@@ -197,3 +197,15 @@ def test_grouped_columns_in_turns(gpu, counts, blocks):
     """More blocks of columns than the waves hold at once."""
     for gated in (False, True):
         layer._grouped_case(np.random.default_rng(blocks), counts, 11, 64, 128 * blocks, "relu", gated, True, gated, "fp32")
+
+
+# ------------------------------------------------------------------ a wave a row of a norm
+@pytest.mark.parametrize("K", [16, 512, 528, 1040, 1536, 2048, 2064, 2560, 2576, 3056, 3088, 3600, 4096, 4112])
+@pytest.mark.parametrize("xt,at,inplace", [("bf16", "bf16", True), ("fp32", "bf16", False), ("bf16", None, False)])
+def test_norm_on_a_wave_a_row(gpu, K, xt, at, inplace):
+    layer._norm_case(np.random.default_rng(K), 1025, K, xt, at, 0, inplace=inplace)
+
+
+@pytest.mark.parametrize("M", [1022, 1023, 1024, 1025, 1026, 1027])
+def test_norm_rows_on_either_side_of_the_rule(gpu, M):
+    layer._norm_case(np.random.default_rng(M), M, 2560, "bf16", "fp32", 0)
