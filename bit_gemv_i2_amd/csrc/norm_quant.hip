@@ -283,16 +283,19 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs p, int hdt) {
             if (p.weight) f[i] *= w[i];
         }
     };
+    // in the last pass over the row, as h_out may be x
+    auto store_h = [&](int v, const float f[8]) {
+        if (!p.h_out) return;
+        if (hdt == BITNET_DT_BF16) store8(static_cast<uint16_t *>(p.h_out) + m * p.K + 8 * v, f);
+        else store8(static_cast<float *>(p.h_out) + m * p.K + 8 * v, f);
+    };
     uint32_t most = 0;
     for (int v = tid; v < n; v += 1024) {
         float f[8];
         normed(v, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) most = max(most, magnitude(f[i]));
-        if (p.h_out) {
-            if (hdt == BITNET_DT_BF16) store8(static_cast<uint16_t *>(p.h_out) + m * p.K + 8 * v, f);
-            else store8(static_cast<float *>(p.h_out) + m * p.K + 8 * v, f);
-        }
+        if (!p.q) store_h(v, f);
     }
     if (!p.q) return;
     most = wave_max(most);
@@ -303,6 +306,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs p, int hdt) {
     for (int v = tid; v < n; v += 1024) {
         float f[8];
         normed(v, f);
+        store_h(v, f);
         *reinterpret_cast<uint2 *>(p.q + m * p.K + 8 * v) = s.codes(f);
     }
     if (tid == 0) p.s_a[m] = s.factor();
@@ -353,6 +357,7 @@ extern "C" bitnet_status_t bitnet_add_norm(const void *x, int xdt, const void *a
     if (M < 1 || M > 65535 * 1024 || (M >= 1 << 22 && K > (slots ? 512 : 4096)) || K < 16 || K % 16 || K > kMaxK ||
         (slots && (parts < 1 || parts > kMaxParts || add_rows < 1)))
         return BITNET_ERR_UNSUPPORTED_SHAPE;
+    if (h_out && (h_out == x_out || (h_out == x && hdt != xdt))) return BITNET_ERR_INVALID_ARG;
     NormArgs p;
     p.x = x; p.add = add; p.slots = slots; p.gates = gates; p.weight = weight; p.x_out = x_out; p.h_out = h_out;
     p.q = q; p.s_a = s_a; p.add_rows = add_rows; p.parts = parts; p.K = K; p.eps = eps;

@@ -562,7 +562,8 @@ bitnet_status_t bitnet_attn_prompt(const void *q, int64_t q_stride, const void *
  *   weight   device, fp32 [K], or NULL for ones
  *   x_out    device, [M][K] of xdt (out); may be x itself, must not overlap add; NULL without add
  *   q, s_a   device, int8 [M][K] and fp32 [M] (out), or both NULL
- *   h_out    device, [M][K], hdt BITNET_DT_BF16 or BITNET_DT_F32 (out), or NULL
+ *   h_out    device, [M][K], hdt BITNET_DT_BF16 or BITNET_DT_F32 (out), or NULL; may be x itself when of the same type and x_out is not
+ * Outputs overlap no other operand and not one another.
  * A row whose h holds an infinity or a NaN (of x, add, a gate or the weight) has s_a = NaN and codes of 0, so that
  * every product of it is NaN; other rows do not see it.
  * Rules: 1 <= M <= 65535 * 1024, and below 2^22 where K > 4096 or, with slots, K > 512; 16 <= K <= 65536, K % 16 == 0; with slots

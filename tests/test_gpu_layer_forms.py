@@ -209,3 +209,27 @@ def test_norm_on_a_wave_a_row(gpu, K, xt, at, inplace):
 @pytest.mark.parametrize("M", [1022, 1023, 1024, 1025, 1026, 1027])
 def test_norm_rows_on_either_side_of_the_rule(gpu, M):
     layer._norm_case(np.random.default_rng(M), M, 2560, "bf16", "fp32", 0)
+
+
+@pytest.mark.parametrize("K", [400, 2560, 16400, 32768, 32784, 65536])
+@pytest.mark.parametrize("M", [3, 1030])
+@pytest.mark.parametrize("added", [False, True])
+def test_norm_into_the_stream_it_reads(gpu, K, M, added):
+    """h_out is x, with the codes of the same call: they are those of the values that x held."""
+    import bit_gemv_i2_amd as bn
+    if M * K > 1 << 24:
+        M = 2
+    rng = np.random.default_rng(K)
+    x, xv = layer._values(rng, (M, K), torch.float32)
+    add, av = layer._values(rng, (M, K), torch.bfloat16)
+    w = (1 + 0.2 * rng.standard_normal(K)).astype(np.float32)
+    stream, h, codes, s_a = lo.add_norm(xv, w, 1e-5, torch.float32, av if added else None)
+    q, s, out, wd = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda"), torch.empty_like(x), layer._dev(w)
+    st = bn.lib().bitnet_add_norm(x.data_ptr(), bn.BITNET_DT_F32, add.data_ptr() if added else None, bn.BITNET_DT_BF16, 0, None, None, 0, wd.data_ptr(),
+                                  1e-5, M, K, out.data_ptr() if added else None, q.data_ptr(), s.data_ptr(), x.data_ptr(), bn.BITNET_DT_F32,
+                                  torch.cuda.current_stream().cuda_stream)
+    assert st == bn.BITNET_OK
+    assert np.array_equal(s.cpu().numpy(), s_a) and np.array_equal(q.cpu().numpy(), codes)
+    assert np.array_equal(x.cpu().numpy(), h)
+    if added:
+        assert np.array_equal(out.cpu().numpy(), stream)
