@@ -3,12 +3,13 @@
 //     v = x + d;  x_out = v in x's type;  r = 1 / sqrt(mean x_out^2 + eps);  h = (x_out r) w;  q = rint(h 127 / max|h|)
 //
 // A row stays in registers between its reads and its writes, so x, the rows of add and the weight are read once and x_out, q
-// written once.  The mean of the squares is summed in 64 bits (squares of fp32 values are exact there): its rounding to fp32, and
-// with it every code, does then not depend on how a row is cut over lanes.
+// written once.  The mean of the squares is summed in 64 bits (squares of fp32 values are exact there).  How a row is cut over lanes
+// moves the last bits of that sum, some 2^-50 of it, which reaches the factor r in fp32 only where it lies that near to a rounding
+// border: about one row in 2^26.
 //
-// Floor: those bytes at a large copy's 5.07 TB/s.  16383 x 2560 bf16 with an addition: 294 MB, 53 to 55 us, 5.3 to 5.5 TB/s, bound by bytes.  512
-// rows of 6 parts each: 27.6 MB, 7.7 us in a graph (5.4 at a copy's rate), bound by the chain of a row: slots, then parts, two
-// reductions, codes.  One row 2.9 us: a launch and that chain.
+// Measured against a large copy's 5.07 TB/s.  16383 x 2560 bf16 with an addition: 294 MB, 53 to 55 us, 5.3 to 5.5 TB/s (it reads more than
+// it writes), bound by bytes.  512 rows of 6 parts each: 27.6 MB, 7.7 us in a graph (5.4 at a copy's rate), bound by the chain of a
+// row: slots, then parts four at a time, two reductions, codes; waves wait in 70% of their time.  One row 2.9 us: a launch and that chain.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

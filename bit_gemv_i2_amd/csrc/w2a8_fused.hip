@@ -29,11 +29,11 @@ __device__ __forceinline__ v4i mfma_i8(v4i a, v4i b, v4i c) { return __builtin_a
 // lane has requested all its codes and scales (streaming loads: nobody reads them again) before the first product.  A wave
 // brings its slice of up to TOK tokens through LDS (a few wide loads instead of many narrow ones; it reads only what it wrote itself,
 // so no barrier), multiplies, and the waves' sums are joined in LDS in a fixed order.  Further tokens of the expert, TOK at a
-// time, meet the codes still in registers.  By expert, workgroup row y has the y-th expert that has any rows, so that no
-// more than there are slots are launched.
+// time, meet the codes still in registers; with more blocks than the waves hold at once (MULTI, above 96) every pass reads them again.
+// By expert, workgroup row y has the y-th expert that has any rows, so that no more than there are slots are launched.
 //
-// Floor: the weights once (9 bits of 32 a weight: 2560 x 6912 5 MB, 13824 x 2560 10 MB; 0.8 and 1.6 us at a bare read's 6.3 TB/s) and a
-// launch.  Measured in a graph, weights from HBM: 1 token x 2560 x 6912 4.1 us, 8 x 13824 x 2560 gated 5.7, 16 tokens 6.4, 1 x
+// Floor: the weights once (9/32 of a byte each, their scales among it: 2560 x 6912 5 MB, 13824 x 2560 10 MB; 0.8 and 1.6 us at a bare
+// read's 6.3 TB/s) and a launch.  Measured in a graph, weights from HBM: 1 token x 2560 x 6912 4.1 us, 8 x 13824 x 2560 gated 5.7, 16 tokens 6.4, 1 x
 // 131072 x 2560 19.6 (4.8 TB/s).  What bounds it: few tiles, one workgroup's chain (launch, loads, products, join); many tiles, the
 // time in which a workgroup has no weights in flight (its start, join and end: half of some 4 us).
 // ==========================================================================
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void rows_kernel(RowsArgs a) {
 // Few rows each of many experts: more tiles of 16 rows than waves fit on the chip.  A workgroup of 4 waves brings up to 16 rows of its
 // expert to LDS whole; then every wave runs through row tiles of its own, all of K each, a chunk of NB blocks in hand and the next one
 // (of the next tile where this one ends) on its way, so that the stream of weights never pauses for a row's index, an activation
-// or an epilogue.
+// or an epilogue.  An expert with more than 16 rows takes a pass over all its weights for each 16.
 // ==========================================================================
 struct StreamArgs {
     FusedArgs p;
@@ -433,6 +433,9 @@ void run_rows(const FusedArgs &p, int gated, hipStream_t stream) {
     // Waves in fours, so that the SIMDs have as many each, of 4 to 8 blocks: 8 x 13824 x 2560 gated 5.7 us with 4 waves, 6.1 with 3, 5.9 with 5,
     // 7.0 with 10; 8 x 20480 x 3200 7.9 with 4, 9.6 with 5, 9.2 with 7; 16 x 2560 x 6912 5.6 with 8, 7.0 with 4, 6.1 with 11.  Two for
     // short columns: 64 experts of 2560 x 1280 16.0 with 2, 20.8 with 4.
+    //     From 64 blocks on the rule fits one token and not several: 1 x 2560 x 13824 6.2 us, with 4 waves in turns 8.6; 1 x 13824 x 11008 gated 12.5
+    // and 14.0; but 8 x 13824 x 8192 gated 12.6 and 11.5, 16 x 13824 x 11008 gated 24.3 and 17.8, 16 x 5120 x 13824 27.6 and 15.2, since
+    // from 65 on 16 tokens of 9 to 12 waves do not fit in LDS and every product is done in passes of 8.
     a.waves = blocks > 12 ? min((over(8) + 3) / 4 * 4, kMostWaves) : blocks > 3 ? 2 : 1;
     a.per = over(a.waves);
     a.waves = over(a.per);
@@ -446,10 +449,14 @@ void run_rows(const FusedArgs &p, int gated, hipStream_t stream) {
 
 // Whether the tiles of w2a8_tiles.hip take it.
 //     By expert (rows or stream against tiles): 12 rows, 64 experts of 2560 x 1280 24.1 us against 31.6, 24 rows 39.8 against 34.4; 16 rows, 8 experts
-// of 6912 x 2560 22.6 against 20.4, of 2560 x 6912 32.5 against 32.6, 32 rows 30.8 against 26.9 and 46.3 against 33.1.
+// of 6912 x 2560 22.6 against 20.4, of 2560 x 6912 32.5 against 32.6, 32 rows 30.8 against 26.9 and 46.3 against 33.1.  The host knows
+// the mean alone, and these are even plans.  Where one expert has most of the rows its passes of 16 follow one another: 900 rows to 64
+// experts of 2560 x 1280 19.4 us, with 100 of them at one expert 63, 225 122, 450 229; 128 rows to 8 of 6912 x 2560 14.4, with 64 at one
+// 38, 120 70.
 //     Else by passes of 16 tokens and tiles of 16 rows a CU, which is what rows cost, while tiles of this few tokens take the time of one chain over
 // K: 2560 x 2560 64 tokens 9.5 us against 17.0, 128 17.0 against 17.5; 13824 x 2560 gated 64 15.7 against 17.0, 80 18.3 against 16.8; 20480 x
-// 3200 32 17.9 against 19.4, 40 24.8 against 19.7; 65536 x 2560 32 37.4 against 23.2; 2560 x 6912 128 26.7 against 31.8.
+// 3200 32 17.9 against 19.4, 40 24.8 against 19.7; 65536 x 2560 32 37.4 against 23.2; 2560 x 6912 128 26.7 against 31.8.  Where neither form suits,
+// bitnet_w2a8_gemm, which has no epilogue, is the faster product: 13824 x 2560 from 40 to 128 tokens, narrow matrices to 512.
 bool many(int64_t slots, int experts, bool grouped, int N) {
     if (grouped) return slots > 16ll * experts;
     const int64_t passes = (slots + 15) / 16;

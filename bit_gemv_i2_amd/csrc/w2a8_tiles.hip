@@ -1,9 +1,10 @@
 // Products with epilogues over many rows, on the matrix cores' 6-bit and 4-bit formats.
 //
-// An int8 activation is two digits, q = 16 h + l with -8 <= h, l <= 8, whole numbers that the 6-bit format (3 exponent, 2
-// mantissa bits) holds exactly; a ternary weight is a 4-bit float (0 or +-2) whose two upper bits are its 2-bit code.  One
-// v_mfma_scale_f32_32x32x64 multiplies 32 tokens by 32 rows over 64 columns; the scale operand gives the upper digits their 16 and the
-// weights' 2 its half.  Block sums are whole numbers below 2^24, so they are exact in fp32 and come out the same as int8
+// An int8 activation is two digits, q = 16 h + l with -8 <= h, l <= 8.  The 6-bit format (3 exponent, 2 mantissa bits) holds the upper
+// digit as h and the lower one as l / 16, both exactly, so that their sum is q / 16; a ternary weight t is the 4-bit float 2 t, whose two
+// upper bits are its 2-bit code.  One 32x32x64 step in mixed formats, without scale operands, multiplies 32 tokens by 32 rows over 64
+// columns, and the steps of both digits add up to sums of q t / 8, which the epilogue multiplies by 8.  Eight times a block's sum is a
+// whole number below 2^24, so block sums are exact in fp32 and come out the same as int8
 // products' (checked bit for bit), at the same rate as int8.  What it saves is everything beside the matrix cores: a block
 // sum needs no conversion before its scale (one fused multiply-add an output and block instead of two operations), 16 codes
 // become operands in three operations instead of seven, and the 32 x 32 shape leaves a wave room for 4 to 6 vector operations
@@ -14,10 +15,12 @@
 //
 // Measured, digits and products together: 8192 tokens x 6912 x 2560, gated, 165 to 175 us, 1.66 to 1.76 POP/s (the plain product's
 // kernel 192 to 198 us; a large int8 library product runs at 2.55 POP/s); 512 x 13824 x 2560 30 us (30), 256
-// tokens 19.5 (21.7).  Four steps a 32 x 32 block, two digits each of two halves, are what int8 takes too.  What bounds it with many tiles is the
-// matrix cores' clock and issue: a step is 14.3 ns with 32 workgroups on the card and 20 to 23 with all 512, whatever else the
-// waves do; of 4095 tokens' 357 thousand cycles the cores are busy in 40%, a wave waits for its turn in 32%, for
-// data or the barrier in 24%; LDS has no bank conflicts.  With few tiles it is one workgroup's chain of blocks, prologue and
+// tokens 19.5 (21.7).  Four steps a 32 x 32 block, two digits each of two halves, are what int8 takes too.  What bounds it with many tiles is
+// that its parts overlap too little, no unit being full: of the cycles in which a CU has work (4095 tokens by expert) the matrix cores
+// are busy in 48%, the vector units in 54% (matrix steps' issue among them), LDS's reads and writes in 28% (direct loads not counted, no
+// bank conflicts); a wave waits for its turn in 32% of its time and for data or the barrier in 24%.  Each block begins with a barrier and 18 LDS
+// reads before its first step.  A step that takes 14.3 ns with 32 workgroups on the card takes 20 to 23 with all 512, which with 4420 steps
+// a SIMD is 88 to 102 of the products' 170 us.  With few tiles it is one workgroup's chain of blocks, prologue and
 // epilogue (1.4 us).  Raising waves' priorities in turn, touching the weights' lines ahead and parting the
 // direct loads among the steps changed nothing.
 #include "fused.h"

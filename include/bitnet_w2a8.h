@@ -574,7 +574,7 @@ bitnet_status_t bitnet_add_norm(const void *x, int xdt, const void *add, int adt
                                 int M, int K, void *x_out, int8_t *q, float *s_a, void *h_out, int hdt,
                                 hipStream_t stream);
 
-/* Activations of the products below, in fp32. */
+/* Activations of the products below, in fp32 as written: where the exponential overflows (SILU below -88.7), the result is -0. */
 typedef enum {
     BITNET_ACT_NONE = 0,
     BITNET_ACT_RELU = 1,  /* max(z, 0) */
