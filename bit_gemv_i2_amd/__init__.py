@@ -871,7 +871,7 @@ def bitnet_add_norm_quant(x, weight=None, eps: float = 1e-5, add=None, slots=Non
 def bitnet_add_norm(x, weight=None, eps: float = 1e-5, add=None, slots=None, gates=None, x_out=None, out_dtype=None, h=None,
                     stream=None):
     """bitnet_add_norm_quant without the quantiser, as before a product of other types: returns (h [M][K] in out_dtype,
-    x's by default, and the new stream)."""
+    x's by default, and the new stream).  x itself serves as h where it is not x_out."""
     _, _, h, x_out = _add_norm("bitnet_add_norm", x, weight, eps, add, slots, gates, x_out, None, None, h,
                                out_dtype or (x.dtype if h is None else h.dtype), stream)
     return h, x_out
